@@ -339,6 +339,117 @@ MOE_API moe_status_t moe_act_quant_mxfp4(const float* in, int32_t rows, int32_t 
 MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_t rows,
                               int32_t K, float* out, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * 8-bit layers: E4M3 weights with one float32 scale per 128 x 128 block, E4M3
+ * activations with one float32 scale per row and 128 consecutive values.  Such
+ * weights come with the layers around the MXFP4 experts (dense projections, the
+ * shared expert) and with checkpoints whose routed experts are 8-bit.  The
+ * pages have no counterpart: they name MXFP4 and int8 paths only.
+ *
+ *   rows     codes [rows, K] u8, scales [rows, ceil(K / 128)] f32
+ *   matrices codes [E, N, K] u8, scales [E, ceil(N / 128), ceil(K / 128)] f32
+ *
+ * The last block of a dimension may be short.  A value is code times scale; a
+ * product sums each block of 128 in the tensor core's float32 accumulator and
+ * the blocks, times both scales, in float32, in ascending order (in up to 8
+ * ranges of K, added in order, when there are few rows).  Quantised outputs
+ * take s = max(max|v| / 448, 2^-126) over a block's values that are not NaN,
+ * and code = E4M3(v / s), rounded to nearest even; a NaN stays NaN.
+ *
+ * K (and the width of quantised outputs) is a multiple of 16 in [16, 65536],
+ * N in [1, 65536], rows up to 2^21, E up to 1024; pointers 16-byte aligned.
+ * Zero rows are allowed and write nothing.  `ws` is a zeroed workspace
+ * (moe_workspace_init) of at least MOE_FP8_STATUS_BYTES bytes that holds the
+ * latched error and the wait limit (moe_get_error, moe_workspace_set_limits)
+ * and no scratch: calls on different streams may share it unless stated
+ * otherwise.  Outputs must not overlap inputs unless stated otherwise.
+ * ------------------------------------------------------------------------- */
+#define MOE_FP8_STATUS_BYTES 128
+
+/* Element types of the 8-bit layers' 16- and 32-bit tensors. */
+#define MOE_DTYPE_BF16 0
+#define MOE_DTYPE_F16 1
+#define MOE_DTYPE_F32 2
+
+/* Device pointers to n_experts 8-bit experts: gate / up matrices [n, I, H],
+ * down [n, H, I], in the layout above. */
+typedef struct moe_fp8_experts {
+  const uint8_t* gate_q;
+  const float* gate_s;
+  const uint8_t* up_q;
+  const float* up_s;
+  const uint8_t* down_q;
+  const float* down_s;
+  int32_t n_experts;
+} moe_fp8_experts_t;
+
+/* Root-mean-square norm of token rows with the residual's addition, quantised:
+ *   v = x + residual (x alone when residual is NULL)
+ *   n = v / sqrt(mean(v^2) + eps) * weight                        [rows, H]
+ *   residual_out = v, y_out = n (either may be NULL), q_out / s_out = n quantised
+ * x, residual, residual_out and y_out have type `dtype`, weight [H] is float32;
+ * everything is computed in float32 from the inputs and each output is rounded
+ * once (the norm sees the sum before it is rounded to residual_out).
+ * residual_out may be residual or x itself, y_out may be x.  16 <= H <= 16384,
+ * H % 16 == 0.  A row whose sum of squares exceeds float32 comes out as zeros. */
+MOE_API moe_status_t moe_rmsnorm_quant_fp8(const void* x, const void* residual, const float* weight,
+                                           int32_t rows, int32_t H, int32_t dtype, float eps,
+                                           void* residual_out, void* y_out, uint8_t* q_out,
+                                           float* s_out, void* stream);
+
+/* out[rows, N] = A [rows, K] W^T, W [N, K] (one matrix), rounded to out_dtype. */
+MOE_API moe_status_t moe_gemm_fp8(const uint8_t* a_q, const float* a_s, const uint8_t* w_q,
+                                  const float* w_s, int32_t rows, int32_t N, int32_t K,
+                                  int32_t out_dtype, void* out, void* ws, size_t ws_bytes,
+                                  void* stream);
+
+/* Products grouped by expert over moe_bucket's offsets [E + 1] and entries
+ * [n_pairs]: for every expert e and bucket position p in
+ * [offsets[e], offsets[e+1]),
+ *   out[scatter ? entries[p] : p] = A[a_div > 0 ? entries[p] / a_div : p] W[e]^T.
+ * a_div = k picks token rows (A [T, K]), a_div = 0 takes rows in bucket order
+ * (A [n_pairs, K] or more rows), a_div = 1 rows in pair order.  entries may be
+ * NULL when neither a_div nor scatter needs it.  Positions outside
+ * [offsets[0], offsets[E]) are left as they were.  Offsets that descend or
+ * leave [0, n_pairs] latch MOE_ERR_DEVICE_DATA and nothing is written; an entry
+ * that names no row latches it and its row is skipped.  Entries are distinct
+ * (with scatter, pairs listed twice race). */
+MOE_API moe_status_t moe_grouped_gemm_fp8(const uint8_t* a_q, const float* a_s, int32_t a_rows,
+                                          const uint8_t* w_q, const float* w_s,
+                                          const int32_t* offsets, const int32_t* entries,
+                                          int32_t n_pairs, int32_t E, int32_t N, int32_t K,
+                                          int32_t a_div, int32_t scatter, int32_t out_dtype,
+                                          void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* The gate / up pair with its SwiGLU, grouped the same way: at bucket position p
+ *   h = silu(A[..] W_gate[e]^T) * (A[..] W_up[e]^T)                        [I]
+ * quantised to q_out [n_pairs, I], s_out [n_pairs, ceil(I / 128)] in bucket
+ * order (what moe_grouped_gemm_fp8 takes with a_div = 0).  I % 16 == 0.
+ * offsets may be NULL with E = 1: one group of all n_pairs rows. */
+MOE_API moe_status_t moe_grouped_swiglu_fp8(const uint8_t* a_q, const float* a_s, int32_t a_rows,
+                                            const uint8_t* gate_q, const float* gate_s,
+                                            const uint8_t* up_q, const float* up_s,
+                                            const int32_t* offsets, const int32_t* entries,
+                                            int32_t n_pairs, int32_t E, int32_t I, int32_t H,
+                                            int32_t a_div, uint8_t* q_out, float* s_out, void* ws,
+                                            size_t ws_bytes, void* stream);
+
+/* moe_expert_ffn_mxfp4 for 8-bit experts and quantised token rows x_q [T, H],
+ * x_s (moe_rmsnorm_quant_fp8): the same partial_out rows, from the same
+ * offsets and entries; h is quantised between the projections.  Shapes as for
+ * moe_expert_ffn_mxfp4.  ws holds h: at least
+ * moe_expert_ffn_fp8_workspace_bytes bytes, calls sharing it ordered on one
+ * stream. */
+MOE_API moe_status_t moe_expert_ffn_fp8(const moe_fp8_experts_t* experts,
+                                        const moe_fp8_experts_t* shared, const uint8_t* x_q,
+                                        const float* x_s, const int32_t* offsets,
+                                        const int32_t* entries, moe_shape_t shape,
+                                        float* partial_out, void* ws, size_t ws_bytes,
+                                        void* stream);
+
+/* Bytes of workspace of moe_expert_ffn_fp8; 0 for an unsupported shape. */
+MOE_API size_t moe_expert_ffn_fp8_workspace_bytes(moe_shape_t shape, int32_t has_shared);
+
 /* Synchronise `stream`, return the first device-side error latched in ws
  * since the last call (MOE_OK if none) and clear it. */
 MOE_API moe_status_t moe_get_error(void* ws, void* stream);

@@ -1,0 +1,227 @@
+// Internal declarations of the E4M3 (block-of-128 scales) operators: argument
+// blocks, launchers, and the sm_100a primitives their kernels use.
+#pragma once
+
+#include <cuda.h>
+
+#include "moe_internal.cuh"
+
+namespace moe {
+
+constexpr int kFp8Block = 128;          // values that share a scale, in both directions
+constexpr float kFp8Max = 448.f;        // largest E4M3 magnitude
+constexpr float kFp8MinScale = 1.17549435e-38f;  // 2^-126: a block of zeros gets codes 0 and this scale
+
+__host__ __device__ inline int fp8_blocks(int n) { return (n + kFp8Block - 1) / kFp8Block; }
+
+// Scale of a block from its largest magnitude (float32, correctly rounded).
+__device__ __forceinline__ float fp8_scale(float amax) {
+  return fmaxf(amax / kFp8Max, kFp8MinScale);
+}
+
+// Two floats -> two E4M3 codes (lo in the low byte), round to nearest even,
+// saturating at +-448, NaN kept.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d) {
+  return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+}
+
+// ---------------------------------------------------------------- launchers ---
+struct NormFp8Args {
+  const void* x;
+  const void* residual;   // or nullptr
+  const float* weight;
+  void* residual_out;     // or nullptr (same storage as residual or x allowed)
+  void* y;                // or nullptr
+  uint8_t* q;
+  float* s;
+  int rows, H, dtype;
+  float eps;
+};
+cudaError_t launch_norm_fp8(const NormFp8Args& a, cudaStream_t st);
+
+// One grouped (or, without offsets, single-group) product; swiglu: gate / up
+// pair with an E4M3 result.
+struct Fp8GemmArgs {
+  const uint8_t* a_q;
+  const float* a_s;       // [a_rows, blocks(K)]
+  const uint8_t* w_q[2];  // [E, N, K]: the weights; or gate and up
+  const float* w_s[2];    // [E, blocks(N), blocks(K)]
+  const int32_t* offsets; // [E + 1], or nullptr: one group of all P rows
+  const int32_t* entries; // [P], or nullptr when neither gathered nor scattered
+  void* out;              // [P, N] out_type
+  uint8_t* q_out;         // swiglu: [P, N], in bucket order
+  float* s_out;           // swiglu: [P, blocks(N)]
+  int* err;
+  int a_rows, P, E, N, K;
+  int a_div;              // > 0: row p of the buckets is A row entries[p] / a_div; 0: row p
+  int scatter;            // output row entries[p] instead of p
+  int out_type;
+};
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, bool swiglu, cudaStream_t st);
+
+// 2-D map of a [rows, row_bytes] uint8 matrix, boxes of box_rows x box_bytes
+// (64 or 128) with the swizzle of the same width.
+bool make_tma_map_u8_box(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                         uint32_t box_bytes, uint32_t box_rows);
+
+// --------------------------------------------------------------- primitives ---
+__device__ __forceinline__ uint32_t smem_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ unsigned long long global_ns() {
+  unsigned long long t;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ void bar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bar_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+// What a role needs to give up a wait: the CTA's abort flag, the error words
+// and the limit.
+struct WaitCtl {
+  volatile int* abort_flag;
+  int* err;
+  unsigned long long limit_ns;
+};
+// Bounded wait; false if it gave up (or another role already did).
+__device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const WaitCtl& c, int where) {
+  if (bar_try(bar, parity)) return true;
+  const unsigned long long t0 = global_ns();
+  while (!bar_try(bar, parity)) {
+    if (*c.abort_flag) return false;
+    if (global_ns() - t0 > c.limit_ns) {
+      *c.abort_flag = 1;
+      latch_error(c.err, MOE_ERR_TIMEOUT, where);
+      return false;
+    }
+  }
+  return true;
+}
+// The same for a whole warp: lane 0 waits, every lane gets the outcome.
+__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& c, int where) {
+  int ok = 0;
+  if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, c, where);
+  return __shfl_sync(kFull, ok, 0) != 0;
+}
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+// Four rows of the matrix (a map with one-row boxes) into four consecutive
+// rows of the tile.
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, int x, int r0, int r1,
+                                            int r2, int r3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tcgen_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tcgen_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tcgen_commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+               : "memory");
+}
+// D (TMEM, float32) = A x B^T (+ D): E4M3 operands in shared memory, K = 32.
+__device__ __forceinline__ void mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
+      "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// K-major operand, 128-byte swizzle, rows of 128 bytes, 8-row groups 1024
+// bytes apart.
+__device__ __forceinline__ uint64_t desc_k_sw128(uint32_t addr) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+// Instruction descriptor: E4M3 x E4M3 -> float32, both K-major, M x N.
+__host__ __device__ constexpr uint32_t idesc_e4m3(int m, int n) {
+  return (1u << 4) | (uint32_t(n >> 3) << 17) | (uint32_t(m >> 4) << 24);
+}
+// 32 columns of this warp's TMEM quarter -> registers (complete on return).
+__device__ __forceinline__ void tmem_load32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// (acc.lo, acc.hi) += (d.lo, d.hi) * s, one rounding each
+__device__ __forceinline__ void fma_pair(float2& acc, uint32_t d0, uint32_t d1, float2 s) {
+  unsigned long long a, d, m;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(acc.x), "f"(acc.y));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(d0), "r"(d1));
+  asm("mov.b64 %0, {%1, %2};" : "=l"(m) : "f"(s.x), "f"(s.y));
+  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(a) : "l"(d), "l"(m));
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(acc.x), "=f"(acc.y) : "l"(a));
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %cluster_nctarank;" : "=r"(r));
+  return r;
+}
+// Every thread of every CTA of the cluster, with release / acquire ordering.
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Shared-memory address `addr` of CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+}  // namespace moe

@@ -8,6 +8,7 @@ the library has not been built.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -34,6 +35,12 @@ MOE_ACT_MXFP4 = 1
 
 MOE_DEBUG_STARVE_FIRST_WAIT = 1
 
+#: smallest workspace of the 8-bit operators
+MOE_FP8_STATUS_BYTES = 128
+
+#: element types of the 8-bit operators' 16- and 32-bit tensors
+MOE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
 #: every symbol include/moe.h declares
 EXPORTS = (
     "moe_workspace_bytes", "moe_workspace_init", "moe_route_topk", "moe_bucket",
@@ -44,6 +51,8 @@ EXPORTS = (
     "moe_slot_bank_bytes", "moe_slot_bank_create", "moe_slot_bank_destroy", "moe_slot_bank_acquire",
     "moe_slot_bank_experts", "moe_slot_bank_stats", "moe_layer_forward_banked",
     "moe_layer_forward_banked_workspace_bytes",
+    "moe_rmsnorm_quant_fp8", "moe_gemm_fp8", "moe_grouped_gemm_fp8", "moe_grouped_swiglu_fp8",
+    "moe_expert_ffn_fp8", "moe_expert_ffn_fp8_workspace_bytes",
 )
 
 
@@ -65,6 +74,10 @@ class moe_mxfp4_experts_t(ctypes.Structure):
                 ("n_experts", ctypes.c_int32)]
 
 
+class moe_fp8_experts_t(ctypes.Structure):
+    _fields_ = list(moe_mxfp4_experts_t._fields_)
+
+
 _lib = None
 
 
@@ -82,6 +95,7 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     shape = moe_shape_t
     ex = ctypes.POINTER(moe_mxfp4_experts_t)
+    ex8 = ctypes.POINTER(moe_fp8_experts_t)
     sig = {
         "moe_workspace_bytes": (sz, [shape, i32, i32, i32]),
         "moe_workspace_init": (i32, [vp, sz, vp]),
@@ -109,6 +123,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         "moe_workspace_set_limits": (i32, [vp, ctypes.c_uint32, ctypes.c_uint32, vp]),
         "moe_status_string": (ctypes.c_char_p, [i32]),
         "moe_version": (ctypes.c_char_p, []),
+        "moe_rmsnorm_quant_fp8": (i32, [vp, vp, vp, i32, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp]),
+        "moe_gemm_fp8": (i32, [vp, vp, vp, vp, i32, i32, i32, i32, vp, vp, sz, vp]),
+        "moe_grouped_gemm_fp8": (i32, [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, i32, i32,
+                                       vp, vp, sz, vp]),
+        "moe_grouped_swiglu_fp8": (i32, [vp, vp, i32, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                         vp, vp, vp, sz, vp]),
+        "moe_expert_ffn_fp8": (i32, [ex8, ex8, vp, vp, vp, vp, shape, vp, vp, sz, vp]),
+        "moe_expert_ffn_fp8_workspace_bytes": (sz, [shape, i32]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -345,6 +367,191 @@ def moe_decode_mxfp4(q, s, K, out, stream=None):
     rows = q.shape[0]
     _check(load_library().moe_decode_mxfp4(_p(q), _p(s), rows, K, _p(out), _s(stream)),
            "moe_decode_mxfp4")
+
+
+# ------------------------------------------------------- 8-bit operators ---
+# E4M3 codes are torch.float8_e4m3fn or uint8 tensors.  Sizes come from the
+# tensors, so these wrappers check shapes and types as well; a mismatch raises
+# ValueError before anything is launched.
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _b128(n):
+    return (n + 127) // 128
+
+
+def _dtype_of(t, what):
+    code = MOE_DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
+    return code
+
+
+def _dev(*ts):
+    """The tensors' one device, made current for the call when it is not."""
+    dev = ts[0].device
+    for t in ts:
+        if t is not None and t.device != dev:
+            raise ValueError("expected tensors on one device")
+    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return _HERE
+
+
+_HERE = contextlib.nullcontext()
+
+
+def _rows8(q, s, what):
+    _need(q.dtype in _CODES and s.dtype == torch.float32, f"{what}: expected E4M3 codes and float32 scales")
+    _need(q.dim() == 2 and s.shape == (q.shape[0], _b128(q.shape[1])),
+          f"{what}: expected codes [rows, K] and scales [rows, ceil(K / 128)]")
+
+
+def _mats8(q, s, what, K):
+    _need(q.dtype in _CODES and s.dtype == torch.float32, f"{what}: expected E4M3 codes and float32 scales")
+    _need(q.dim() == 3 and q.shape[2] == K and s.shape == (q.shape[0], _b128(q.shape[1]), _b128(K)),
+          f"{what}: expected codes [E, N, K] and scales [E, ceil(N / 128), ceil(K / 128)]")
+
+
+def _groups(offsets, entries, E, n_pairs):
+    for t in (offsets, entries):
+        _need(t is None or t.dtype == torch.int32, "offsets, entries: expected int32")
+    _need(offsets is None or offsets.numel() == E + 1, "offsets: expected E + 1 values")
+    _need(entries is None or entries.numel() == n_pairs, "entries: expected one value per pair")
+
+
+def moe_rmsnorm_quant_fp8(x, weight, eps, q_out, s_out, residual=None, residual_out=None, y_out=None,
+                          stream=None):
+    """Residual addition, root-mean-square norm and E4M3 quantisation of the
+    rows of x [rows, H] (moe.h).  residual_out, y_out may be None."""
+    dt = _dtype_of(x, "x")
+    _need(x.dim() == 2 and q_out.shape == x.shape and weight.shape == x.shape[1:]
+          and weight.dtype == torch.float32, "expected x, q_out [rows, H] and a float32 weight [H]")
+    _rows8(q_out, s_out, "q_out, s_out")
+    for t in (residual, residual_out, y_out):
+        _need(t is None or (t.shape == x.shape and t.dtype == x.dtype),
+              "residual, residual_out, y_out: expected the shape and type of x")
+    with _dev(x, weight, q_out, s_out, residual, residual_out, y_out):
+        _check(load_library().moe_rmsnorm_quant_fp8(
+            _p(x), _p(residual), _p(weight), x.shape[0], x.shape[1], dt, eps, _p(residual_out), _p(y_out),
+            _p(q_out), _p(s_out), _s(stream)), "moe_rmsnorm_quant_fp8")
+
+
+def moe_gemm_fp8(a_q, a_s, w_q, w_s, out, ws, stream=None):
+    """out [rows, N] = A [rows, K] times W [N, K] transposed, both E4M3 with
+    scales per 128 (moe.h); out is bfloat16, float16 or float32."""
+    dt = _dtype_of(out, "out")
+    _rows8(a_q, a_s, "a_q, a_s")
+    rows, K = a_q.shape
+    N = w_q.shape[0]
+    _need(w_q.dtype in _CODES and w_s.dtype == torch.float32 and w_q.shape == (N, K)
+          and w_s.shape == (_b128(N), _b128(K)),
+          "w_q, w_s: expected codes [N, K] and float32 scales [ceil(N / 128), ceil(K / 128)]")
+    _need(out.shape == (rows, N), "out: expected [rows, N]")
+    with _dev(a_q, a_s, w_q, w_s, out, ws):
+        _check(load_library().moe_gemm_fp8(_p(a_q), _p(a_s), _p(w_q), _p(w_s), rows, N, K, dt, _p(out),
+                                           _p(ws), ws.numel() * ws.element_size(), _s(stream)),
+               "moe_gemm_fp8")
+
+
+def moe_grouped_gemm_fp8(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div=0, scatter=False,
+                         stream=None):
+    """Products grouped by expert (moe.h): out [n_pairs, N], w_q [E, N, K],
+    offsets and entries from moe_bucket.  a_div = k takes token rows, 0 rows in
+    bucket order; scatter writes row entries[p] instead of p."""
+    dt = _dtype_of(out, "out")
+    _rows8(a_q, a_s, "a_q, a_s")
+    a_rows, K = a_q.shape
+    _mats8(w_q, w_s, "w_q, w_s", K)
+    E, N, _ = w_q.shape
+    _need(out.dim() == 2 and out.shape[1] == N, "out: expected [n_pairs, N]")
+    P = out.shape[0]
+    _groups(offsets, entries, E, P)
+    with _dev(a_q, a_s, w_q, w_s, offsets, entries, out, ws):
+        _check(load_library().moe_grouped_gemm_fp8(
+            _p(a_q), _p(a_s), a_rows, _p(w_q), _p(w_s), _p(offsets), _p(entries), P, E, N, K, a_div,
+            int(scatter), dt, _p(out), _p(ws), ws.numel() * ws.element_size(), _s(stream)),
+            "moe_grouped_gemm_fp8")
+
+
+def moe_grouped_swiglu_fp8(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws,
+                           a_div=0, stream=None):
+    """Grouped gate / up projections with SwiGLU and E4M3 quantisation (moe.h):
+    q_out [n_pairs, I], s_out [n_pairs, ceil(I / 128)] in bucket order."""
+    _rows8(a_q, a_s, "a_q, a_s")
+    a_rows, H = a_q.shape
+    _mats8(gate_q, gate_s, "gate_q, gate_s", H)
+    _mats8(up_q, up_s, "up_q, up_s", H)
+    E, I, _ = gate_q.shape
+    _need(up_q.shape == gate_q.shape, "up_q: expected the shape of gate_q")
+    _rows8(q_out, s_out, "q_out, s_out")
+    _need(q_out.shape[1] == I, "q_out: expected [n_pairs, I]")
+    P = q_out.shape[0]
+    _groups(offsets, entries, E, P)
+    with _dev(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws):
+        _check(load_library().moe_grouped_swiglu_fp8(
+            _p(a_q), _p(a_s), a_rows, _p(gate_q), _p(gate_s), _p(up_q), _p(up_s), _p(offsets), _p(entries),
+            P, E, I, H, a_div, _p(q_out), _p(s_out), _p(ws), ws.numel() * ws.element_size(), _s(stream)),
+            "moe_grouped_swiglu_fp8")
+
+
+@dataclasses.dataclass
+class Fp8Experts:
+    """Device tensors of n 8-bit experts: codes gate_q / up_q [n, I, H] and
+    down_q [n, H, I] with float32 scales per 128 x 128 block."""
+    gate_q: torch.Tensor
+    gate_s: torch.Tensor
+    up_q: torch.Tensor
+    up_s: torch.Tensor
+    down_q: torch.Tensor
+    down_s: torch.Tensor
+
+    @property
+    def n_experts(self) -> int:
+        return int(self.gate_q.shape[0])
+
+    def cstruct(self) -> moe_fp8_experts_t:
+        _, I, H = self.gate_q.shape
+        _mats8(self.gate_q, self.gate_s, "gate", H)
+        _mats8(self.up_q, self.up_s, "up", H)
+        _mats8(self.down_q, self.down_s, "down", I)
+        _need(self.up_q.shape == self.gate_q.shape and self.down_q.shape == (self.n_experts, H, I),
+              "expected gate, up [n, I, H] and down [n, H, I]")
+        return moe_fp8_experts_t(_p(self.gate_q), _p(self.gate_s), _p(self.up_q), _p(self.up_s),
+                                 _p(self.down_q), _p(self.down_s), self.n_experts)
+
+
+def fp8_workspace(shape: moe_shape_t, has_shared: bool = False, device="cuda", stream=None) -> torch.Tensor:
+    """A zeroed workspace for moe_expert_ffn_fp8 (and the other 8-bit operators)."""
+    n = int(load_library().moe_expert_ffn_fp8_workspace_bytes(shape, int(has_shared)))
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_expert_ffn_fp8_workspace_bytes")
+    ws = torch.empty(n, dtype=torch.uint8, device=device)
+    moe_workspace_init(ws, stream)
+    return ws
+
+
+def moe_expert_ffn_fp8(experts: Fp8Experts, shared, x_q, x_s, offsets, entries, shape, partial_out, ws,
+                       stream=None):
+    """moe_expert_ffn_mxfp4 for 8-bit experts and quantised token rows (moe.h)."""
+    _rows8(x_q, x_s, "x_q, x_s")
+    _need(x_q.shape == (shape.T, shape.H), "x_q: expected [T, H]")
+    for e in (experts, shared):
+        _need(e is None or e.gate_q.shape[1:] == (shape.I, shape.H), "experts: expected gate, up [n, I, H]")
+    _groups(offsets, entries, shape.E, shape.T * shape.k)
+    rows = shape.T * (shape.k + (shared is not None))
+    _need(partial_out.dtype == torch.float32 and partial_out.shape == (rows, shape.H),
+          "partial_out: expected float32 [T k (+ T), H]")
+    with _dev(x_q, x_s, offsets, entries, partial_out, ws, experts.gate_q):
+        _check(load_library().moe_expert_ffn_fp8(_ex(experts), _ex(shared), _p(x_q), _p(x_s), _p(offsets),
+                                                 _p(entries), shape, _p(partial_out), _p(ws),
+                                                 ws.numel() * ws.element_size(), _s(stream)),
+               "moe_expert_ffn_fp8")
 
 
 def moe_get_error(ws, stream=None) -> int:

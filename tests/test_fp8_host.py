@@ -1,0 +1,158 @@
+"""The 8-bit operators on the host: the oracle's E4M3 against torch's, the C
+entry points' refusals and the binding's (no GPU: every call returns or raises
+before anything is launched)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8_oracle as F
+from routed_expert_ffn_fp32_b200 import build, moe
+
+A = 0x100000  # aligned, never dereferenced
+BIG = 1 << 30
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return moe.load_library()
+
+
+def _p(addr=A):
+    return ctypes.c_void_p(addr)
+
+
+def test_e4m3_table_and_rounding_match_torch():
+    codes = np.arange(256, dtype=np.uint8)
+    want = torch.from_numpy(codes).view(torch.float8_e4m3fn).double().numpy()
+    np.testing.assert_array_equal(F.decode(codes), want)
+    rng = np.random.default_rng(0)
+    v = np.concatenate([rng.normal(size=4000) * 2.0 ** rng.integers(-12, 9, 4000),
+                        F.decode(codes[:127]), (F.decode(codes[:126]) + F.decode(codes[1:127])) / 2])
+    v = np.clip(v, -448, 448)
+    got = F.encode(v)
+    # every value here is a float32, so torch's rounding sees it exactly
+    v32 = v.astype(np.float32)
+    want = torch.from_numpy(v32).to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    np.testing.assert_array_equal(F.encode(v32), want)
+    assert (np.abs(F.decode(got) - v) <= np.maximum(np.abs(v) * 2.0 ** -4, 2.0 ** -10)).all()
+    assert F.encode([1e9, -1e9]).tolist() == [0x7E, 0xFE] and F.encode([np.nan])[0] == 0x7F
+
+
+def test_workspace_bytes(lib):
+    s = moe.shape_of(5, 4096, 2048, 256, 8)
+    n = lib.moe_expert_ffn_fp8_workspace_bytes(s, 0)
+    assert n >= 40 * (2048 + 16 * 4) + moe.MOE_FP8_STATUS_BYTES
+    assert lib.moe_expert_ffn_fp8_workspace_bytes(s, 1) >= n + 5 * 2048
+    for bad in [(0, 256, 128, 8, 2), (1, 250, 128, 8, 2), (1, 256, 120, 8, 2), (1, 256, 128, 1025, 2),
+                (1, 256, 128, 8, 17)]:
+        assert lib.moe_expert_ffn_fp8_workspace_bytes(moe.shape_of(*bad), 0) == 0, bad
+
+
+def test_norm_refusals(lib):
+    def call(x=A, res=A, w=A, rows=4, H=256, dt=0, eps=1e-6, ro=A, y=A, q=A, s=A):
+        return lib.moe_rmsnorm_quant_fp8(x, res, w, rows, H, dt, eps, ro, y, q, s, None)
+
+    for kw in [dict(x=None), dict(w=None), dict(q=None), dict(s=None), dict(x=A + 2), dict(res=A + 4),
+               dict(ro=A + 8), dict(y=A + 2), dict(dt=3), dict(dt=-1), dict(eps=-1.0), dict(eps=float("nan"))]:
+        assert call(**kw) == moe.MOE_ERR_INVALID_ARG, kw
+    for kw in [dict(H=0), dict(H=8), dict(H=24), dict(H=16400), dict(rows=-1), dict(rows=(1 << 21) + 1)]:
+        assert call(**kw) == moe.MOE_ERR_UNSUPPORTED_SHAPE, kw
+    assert call(rows=0) == moe.MOE_OK
+
+
+def test_gemm_refusals(lib):
+    def call(aq=A, as_=A, wq=A, ws_=A, rows=4, N=100, K=256, dt=0, out=A, ws=A, n=BIG):
+        return lib.moe_gemm_fp8(aq, as_, wq, ws_, rows, N, K, dt, out, ws, n, None)
+
+    for kw in [dict(aq=None), dict(as_=None), dict(wq=None), dict(ws_=None), dict(out=None), dict(ws=None),
+               dict(aq=A + 8), dict(wq=A + 1), dict(ws_=A + 4), dict(out=A + 2), dict(dt=3)]:
+        assert call(**kw) == moe.MOE_ERR_INVALID_ARG, kw
+    for kw in [dict(rows=-1), dict(rows=(1 << 21) + 1), dict(N=0), dict(N=65537), dict(K=0), dict(K=24),
+               dict(K=65552)]:
+        assert call(**kw) == moe.MOE_ERR_UNSUPPORTED_SHAPE, kw
+    assert call(n=64) == moe.MOE_ERR_WORKSPACE
+    assert call(rows=0) == moe.MOE_OK
+
+
+def test_grouped_refusals(lib):
+    def gemm(aq=A, a_rows=8, off=A, ent=A, P=8, E=4, N=100, K=256, div=0, sc=1, dt=0, out=A, ws=A, n=BIG):
+        return lib.moe_grouped_gemm_fp8(aq, A, a_rows, A, A, off, ent, P, E, N, K, div, sc, dt, out, ws, n, None)
+
+    def swiglu(aq=A, a_rows=8, off=A, ent=A, P=8, E=4, I=128, H=256, div=2, q=A, ws=A, n=BIG):
+        return lib.moe_grouped_swiglu_fp8(aq, A, a_rows, A, A, A, A, off, ent, P, E, I, H, div, q, A, ws, n, None)
+
+    inv, shp = moe.MOE_ERR_INVALID_ARG, moe.MOE_ERR_UNSUPPORTED_SHAPE
+    for kw in [dict(aq=None), dict(off=None), dict(ent=None), dict(out=None), dict(ws=A + 8), dict(div=-1),
+               dict(dt=9), dict(a_rows=7), dict(ent=A + 4), dict(sc=0, div=2, ent=None)]:
+        assert gemm(**kw) == inv, kw
+    for kw in [dict(P=-1), dict(E=0), dict(E=1025), dict(N=0), dict(K=20), dict(a_rows=0)]:
+        assert gemm(**kw) == shp, kw
+    for kw in [dict(aq=A + 2), dict(off=None), dict(ent=None), dict(q=None), dict(div=-2), dict(div=0, a_rows=7)]:
+        assert swiglu(**kw) == inv, kw
+    for kw in [dict(I=120), dict(I=0), dict(H=100), dict(E=2000), dict(P=-1)]:
+        assert swiglu(**kw) == shp, kw
+    assert gemm(n=127) == moe.MOE_ERR_WORKSPACE and swiglu(n=127) == moe.MOE_ERR_WORKSPACE
+    assert gemm(P=0) == moe.MOE_OK and swiglu(P=0, a_rows=0) == moe.MOE_OK
+
+
+def test_expert_ffn_refusals(lib):
+    s = moe.shape_of(4, 256, 128, 8, 2)
+    ex = moe.moe_fp8_experts_t(A, A, A, A, A, A, 8)
+
+    def call(e=ex, sh=None, xq=A, off=A, shape=s, out=A, n=BIG):
+        return lib.moe_expert_ffn_fp8(ctypes.byref(e), None if sh is None else ctypes.byref(sh), xq, A, off, A,
+                                      shape, out, A, n, None)
+
+    assert call(e=moe.moe_fp8_experts_t(A, A, A, A, A, A, 7)) == moe.MOE_ERR_INVALID_ARG
+    assert call(e=moe.moe_fp8_experts_t(A, A, A, None, A, A, 8)) == moe.MOE_ERR_INVALID_ARG
+    assert call(sh=moe.moe_fp8_experts_t(A, A, A, A, A, A, 2)) == moe.MOE_ERR_INVALID_ARG
+    assert call(xq=None) == moe.MOE_ERR_INVALID_ARG and call(off=A + 4) == moe.MOE_ERR_INVALID_ARG
+    assert call(shape=moe.shape_of(4, 256, 120, 8, 2)) == moe.MOE_ERR_UNSUPPORTED_SHAPE
+    assert call(n=200) == moe.MOE_ERR_WORKSPACE
+
+
+def _t(*shape, dtype=torch.uint8):
+    return torch.zeros(shape, dtype=dtype)
+
+
+def test_binding_refuses_shapes_and_types():
+    f32, ws = torch.float32, _t(256)
+    aq, as_ = _t(4, 272), _t(4, 3, dtype=f32)
+    wq, ws_ = _t(100, 272), _t(1, 3, dtype=f32)
+    out = _t(4, 100, dtype=torch.bfloat16)
+    bad = [dict(a_s=_t(4, 2, dtype=f32)), dict(a_q=_t(4, 272, dtype=torch.int8)), dict(w_q=_t(100, 256)),
+           dict(w_s=_t(3, 1, dtype=f32)), dict(out=_t(4, 99, dtype=torch.bfloat16)), dict(out=_t(4, 100)),
+           dict(a_s=_t(4, 3, dtype=torch.float64))]
+    for kw in bad:
+        args = dict(a_q=aq, a_s=as_, w_q=wq, w_s=ws_, out=out, ws=ws) | kw
+        with pytest.raises(ValueError):
+            moe.moe_gemm_fp8(**args)
+    with pytest.raises(ValueError, match="CUDA"):  # right shapes, but host tensors
+        moe.moe_gemm_fp8(aq, as_, wq, ws_, out, ws)
+    off, ent = _t(3, dtype=torch.int32), _t(4, dtype=torch.int32)
+    mq, ms = _t(2, 100, 272), _t(2, 1, 3, dtype=f32)
+    for kw in [dict(offsets=_t(2, dtype=torch.int32)), dict(offsets=_t(3, dtype=torch.int64)),
+               dict(entries=_t(3, dtype=torch.int32)), dict(w_q=_t(2, 100, 256)), dict(out=_t(4, 98, dtype=f32))]:
+        args = dict(a_q=aq, a_s=as_, w_q=mq, w_s=ms, offsets=off, entries=ent, out=out, ws=ws) | kw
+        with pytest.raises(ValueError):
+            moe.moe_grouped_gemm_fp8(**args)
+    gq, gs = _t(2, 128, 272), _t(2, 1, 3, dtype=f32)
+    for kw in [dict(up_q=_t(2, 144, 272), up_s=_t(2, 2, 3, dtype=f32)), dict(q_out=_t(4, 144)),
+               dict(s_out=_t(4, 2, dtype=f32))]:
+        args = dict(a_q=aq, a_s=as_, gate_q=gq, gate_s=gs, up_q=gq, up_s=gs, offsets=off, entries=ent,
+                    q_out=_t(4, 128), s_out=_t(4, 1, dtype=f32), ws=ws) | kw
+        with pytest.raises(ValueError):
+            moe.moe_grouped_swiglu_fp8(**args)
+    x = _t(4, 256, dtype=torch.float16)
+    for kw in [dict(weight=_t(256, dtype=torch.float16)), dict(weight=_t(255, dtype=f32)),
+               dict(x=_t(4, 256, dtype=torch.float64)), dict(residual=_t(4, 256, dtype=f32)),
+               dict(s_out=_t(4, 1, dtype=f32)), dict(y_out=_t(3, 256, dtype=torch.float16))]:
+        args = dict(x=x, weight=_t(256, dtype=f32), eps=1e-6, q_out=_t(4, 256), s_out=_t(4, 2, dtype=f32)) | kw
+        with pytest.raises(ValueError):
+            moe.moe_rmsnorm_quant_fp8(**args)
+    if torch.cuda.is_available():
+        with pytest.raises(ValueError, match="one device"):
+            moe.moe_rmsnorm_quant_fp8(x.cuda(), _t(256, dtype=f32), 1e-6, _t(4, 256), _t(4, 2, dtype=f32))
