@@ -8,7 +8,6 @@ the library has not been built.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import dataclasses
 import os
@@ -372,8 +371,11 @@ def moe_decode_mxfp4(q, s, K, out, stream=None):
 # ------------------------------------------------------- 8-bit operators ---
 # E4M3 codes are torch.float8_e4m3fn or uint8 tensors.  Sizes come from the
 # tensors, so these wrappers check shapes and types as well; a mismatch raises
-# ValueError before anything is launched.
+# ValueError before anything is launched.  A decode step makes many of these
+# calls, so the checks are written to cost little: the wrapper, the launch
+# included, takes about as long as the smallest kernel.
 _CODES = (torch.float8_e4m3fn, torch.uint8)
+_F32 = torch.float32
 
 
 def _need(ok, what):
@@ -392,37 +394,62 @@ def _dtype_of(t, what):
     return code
 
 
-def _dev(*ts):
-    """The tensors' one device, made current for the call when it is not."""
-    dev = ts[0].device
+def _ptrs(*ts):
+    """Device pointers (None stays None) and the tensors' one CUDA device."""
+    dev, out = None, []
     for t in ts:
-        if t is not None and t.device != dev:
-            raise ValueError("expected tensors on one device")
-    if dev.type == "cuda" and dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return _HERE
+        if t is None:
+            out.append(None)
+            continue
+        d = t.get_device()
+        if d != dev:
+            if dev is not None:
+                raise ValueError("expected tensors on one device")
+            if d < 0:
+                raise ValueError("expected CUDA tensors")
+            dev = d
+        if not t.is_contiguous():
+            raise ValueError("expected contiguous tensors")
+        out.append(t.data_ptr())
+    return dev, out
 
 
-_HERE = contextlib.nullcontext()
+def _call(fn, where, dev, stream, args):
+    """fn(*args, stream) on the tensors' device, made current when it is not."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _call(fn, where, dev, stream, args)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream)
+    status = fn(*args, st)
+    if status != MOE_OK:
+        raise MoeError(status, where)
 
 
 def _rows8(q, s, what):
-    _need(q.dtype in _CODES and s.dtype == torch.float32, f"{what}: expected E4M3 codes and float32 scales")
-    _need(q.dim() == 2 and s.shape == (q.shape[0], _b128(q.shape[1])),
-          f"{what}: expected codes [rows, K] and scales [rows, ceil(K / 128)]")
+    """Checks codes [rows, K] and their scales; returns (rows, K)."""
+    if q.dtype not in _CODES or s.dtype is not _F32:
+        raise ValueError(f"{what}: expected E4M3 codes and float32 scales")
+    shape = q.shape
+    if len(shape) != 2 or s.shape != (shape[0], (shape[1] + 127) // 128):
+        raise ValueError(f"{what}: expected codes [rows, K] and scales [rows, ceil(K / 128)]")
+    return shape
 
 
 def _mats8(q, s, what, K):
-    _need(q.dtype in _CODES and s.dtype == torch.float32, f"{what}: expected E4M3 codes and float32 scales")
-    _need(q.dim() == 3 and q.shape[2] == K and s.shape == (q.shape[0], _b128(q.shape[1]), _b128(K)),
-          f"{what}: expected codes [E, N, K] and scales [E, ceil(N / 128), ceil(K / 128)]")
+    """Checks codes [E, N, K] and their scales; returns (E, N, K)."""
+    if q.dtype not in _CODES or s.dtype is not _F32:
+        raise ValueError(f"{what}: expected E4M3 codes and float32 scales")
+    shape = q.shape
+    if len(shape) != 3 or shape[2] != K or s.shape != (shape[0], (shape[1] + 127) // 128, (K + 127) // 128):
+        raise ValueError(f"{what}: expected codes [E, N, K] and scales [E, ceil(N / 128), ceil(K / 128)]")
+    return shape
 
 
 def _groups(offsets, entries, E, n_pairs):
-    for t in (offsets, entries):
-        _need(t is None or t.dtype == torch.int32, "offsets, entries: expected int32")
-    _need(offsets is None or offsets.numel() == E + 1, "offsets: expected E + 1 values")
-    _need(entries is None or entries.numel() == n_pairs, "entries: expected one value per pair")
+    if offsets is not None and (offsets.dtype is not torch.int32 or offsets.numel() != E + 1):
+        raise ValueError("offsets: expected E + 1 int32 values")
+    if entries is not None and (entries.dtype is not torch.int32 or entries.numel() != n_pairs):
+        raise ValueError("entries: expected one int32 value per pair")
 
 
 def moe_rmsnorm_quant_fp8(x, weight, eps, q_out, s_out, residual=None, residual_out=None, y_out=None,
@@ -430,33 +457,33 @@ def moe_rmsnorm_quant_fp8(x, weight, eps, q_out, s_out, residual=None, residual_
     """Residual addition, root-mean-square norm and E4M3 quantisation of the
     rows of x [rows, H] (moe.h).  residual_out, y_out may be None."""
     dt = _dtype_of(x, "x")
-    _need(x.dim() == 2 and q_out.shape == x.shape and weight.shape == x.shape[1:]
-          and weight.dtype == torch.float32, "expected x, q_out [rows, H] and a float32 weight [H]")
-    _rows8(q_out, s_out, "q_out, s_out")
+    shape = x.shape
+    rows, H = _rows8(q_out, s_out, "q_out, s_out")
+    if shape != (rows, H) or weight.shape != (H,) or weight.dtype is not _F32:
+        raise ValueError("expected x, q_out [rows, H] and a float32 weight [H]")
     for t in (residual, residual_out, y_out):
-        _need(t is None or (t.shape == x.shape and t.dtype == x.dtype),
-              "residual, residual_out, y_out: expected the shape and type of x")
-    with _dev(x, weight, q_out, s_out, residual, residual_out, y_out):
-        _check(load_library().moe_rmsnorm_quant_fp8(
-            _p(x), _p(residual), _p(weight), x.shape[0], x.shape[1], dt, eps, _p(residual_out), _p(y_out),
-            _p(q_out), _p(s_out), _s(stream)), "moe_rmsnorm_quant_fp8")
+        if t is not None and (t.shape != shape or t.dtype is not x.dtype):
+            raise ValueError("residual, residual_out, y_out: expected the shape and type of x")
+    dev, (px, pr, pw, pro, py, pq, ps) = _ptrs(x, residual, weight, residual_out, y_out, q_out, s_out)
+    _call((_lib or load_library()).moe_rmsnorm_quant_fp8, "moe_rmsnorm_quant_fp8", dev, stream,
+          (px, pr, pw, rows, H, dt, eps, pro, py, pq, ps))
 
 
 def moe_gemm_fp8(a_q, a_s, w_q, w_s, out, ws, stream=None):
     """out [rows, N] = A [rows, K] times W [N, K] transposed, both E4M3 with
     scales per 128 (moe.h); out is bfloat16, float16 or float32."""
     dt = _dtype_of(out, "out")
-    _rows8(a_q, a_s, "a_q, a_s")
-    rows, K = a_q.shape
-    N = w_q.shape[0]
-    _need(w_q.dtype in _CODES and w_s.dtype == torch.float32 and w_q.shape == (N, K)
-          and w_s.shape == (_b128(N), _b128(K)),
-          "w_q, w_s: expected codes [N, K] and float32 scales [ceil(N / 128), ceil(K / 128)]")
-    _need(out.shape == (rows, N), "out: expected [rows, N]")
-    with _dev(a_q, a_s, w_q, w_s, out, ws):
-        _check(load_library().moe_gemm_fp8(_p(a_q), _p(a_s), _p(w_q), _p(w_s), rows, N, K, dt, _p(out),
-                                           _p(ws), ws.numel() * ws.element_size(), _s(stream)),
-               "moe_gemm_fp8")
+    rows, K = _rows8(a_q, a_s, "a_q, a_s")
+    shape = w_q.shape
+    if len(shape) != 2 or shape[1] != K or w_q.dtype not in _CODES or w_s.dtype is not _F32 \
+            or w_s.shape != ((shape[0] + 127) // 128, (K + 127) // 128):
+        raise ValueError("w_q, w_s: expected codes [N, K] and float32 scales [ceil(N / 128), ceil(K / 128)]")
+    N = shape[0]
+    if out.shape != (rows, N):
+        raise ValueError("out: expected [rows, N]")
+    dev, (pa, pas, pw, pws, po, pk) = _ptrs(a_q, a_s, w_q, w_s, out, ws)
+    _call((_lib or load_library()).moe_gemm_fp8, "moe_gemm_fp8", dev, stream,
+          (pa, pas, pw, pws, rows, N, K, dt, po, pk, ws.nbytes))
 
 
 def moe_grouped_gemm_fp8(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div=0, scatter=False,
@@ -465,39 +492,34 @@ def moe_grouped_gemm_fp8(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div=0,
     offsets and entries from moe_bucket.  a_div = k takes token rows, 0 rows in
     bucket order; scatter writes row entries[p] instead of p."""
     dt = _dtype_of(out, "out")
-    _rows8(a_q, a_s, "a_q, a_s")
-    a_rows, K = a_q.shape
-    _mats8(w_q, w_s, "w_q, w_s", K)
-    E, N, _ = w_q.shape
-    _need(out.dim() == 2 and out.shape[1] == N, "out: expected [n_pairs, N]")
-    P = out.shape[0]
+    a_rows, K = _rows8(a_q, a_s, "a_q, a_s")
+    E, N, _ = _mats8(w_q, w_s, "w_q, w_s", K)
+    shape = out.shape
+    if len(shape) != 2 or shape[1] != N:
+        raise ValueError("out: expected [n_pairs, N]")
+    P = shape[0]
     _groups(offsets, entries, E, P)
-    with _dev(a_q, a_s, w_q, w_s, offsets, entries, out, ws):
-        _check(load_library().moe_grouped_gemm_fp8(
-            _p(a_q), _p(a_s), a_rows, _p(w_q), _p(w_s), _p(offsets), _p(entries), P, E, N, K, a_div,
-            int(scatter), dt, _p(out), _p(ws), ws.numel() * ws.element_size(), _s(stream)),
-            "moe_grouped_gemm_fp8")
+    dev, (pa, pas, pw, pws, pf, pe, po, pk) = _ptrs(a_q, a_s, w_q, w_s, offsets, entries, out, ws)
+    _call((_lib or load_library()).moe_grouped_gemm_fp8, "moe_grouped_gemm_fp8", dev, stream,
+          (pa, pas, a_rows, pw, pws, pf, pe, P, E, N, K, a_div, scatter, dt, po, pk, ws.nbytes))
 
 
 def moe_grouped_swiglu_fp8(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws,
                            a_div=0, stream=None):
     """Grouped gate / up projections with SwiGLU and E4M3 quantisation (moe.h):
     q_out [n_pairs, I], s_out [n_pairs, ceil(I / 128)] in bucket order."""
-    _rows8(a_q, a_s, "a_q, a_s")
-    a_rows, H = a_q.shape
-    _mats8(gate_q, gate_s, "gate_q, gate_s", H)
-    _mats8(up_q, up_s, "up_q, up_s", H)
-    E, I, _ = gate_q.shape
-    _need(up_q.shape == gate_q.shape, "up_q: expected the shape of gate_q")
-    _rows8(q_out, s_out, "q_out, s_out")
-    _need(q_out.shape[1] == I, "q_out: expected [n_pairs, I]")
-    P = q_out.shape[0]
+    a_rows, H = _rows8(a_q, a_s, "a_q, a_s")
+    E, I, _ = shape = _mats8(gate_q, gate_s, "gate_q, gate_s", H)
+    if _mats8(up_q, up_s, "up_q, up_s", H) != shape:
+        raise ValueError("up_q: expected the shape of gate_q")
+    P, width = _rows8(q_out, s_out, "q_out, s_out")
+    if width != I:
+        raise ValueError("q_out: expected [n_pairs, I]")
     _groups(offsets, entries, E, P)
-    with _dev(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws):
-        _check(load_library().moe_grouped_swiglu_fp8(
-            _p(a_q), _p(a_s), a_rows, _p(gate_q), _p(gate_s), _p(up_q), _p(up_s), _p(offsets), _p(entries),
-            P, E, I, H, a_div, _p(q_out), _p(s_out), _p(ws), ws.numel() * ws.element_size(), _s(stream)),
-            "moe_grouped_swiglu_fp8")
+    dev, (pa, pas, pg, pgs, pu, pus, pf, pe, pq, ps, pk) = _ptrs(
+        a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws)
+    _call((_lib or load_library()).moe_grouped_swiglu_fp8, "moe_grouped_swiglu_fp8", dev, stream,
+          (pa, pas, a_rows, pg, pgs, pu, pus, pf, pe, P, E, I, H, a_div, pq, ps, pk, ws.nbytes))
 
 
 @dataclasses.dataclass
@@ -547,11 +569,9 @@ def moe_expert_ffn_fp8(experts: Fp8Experts, shared, x_q, x_s, offsets, entries, 
     rows = shape.T * (shape.k + (shared is not None))
     _need(partial_out.dtype == torch.float32 and partial_out.shape == (rows, shape.H),
           "partial_out: expected float32 [T k (+ T), H]")
-    with _dev(x_q, x_s, offsets, entries, partial_out, ws, experts.gate_q):
-        _check(load_library().moe_expert_ffn_fp8(_ex(experts), _ex(shared), _p(x_q), _p(x_s), _p(offsets),
-                                                 _p(entries), shape, _p(partial_out), _p(ws),
-                                                 ws.numel() * ws.element_size(), _s(stream)),
-               "moe_expert_ffn_fp8")
+    dev, (px, pxs, pf, pe, po, pk, _) = _ptrs(x_q, x_s, offsets, entries, partial_out, ws, experts.gate_q)
+    _call(load_library().moe_expert_ffn_fp8, "moe_expert_ffn_fp8", dev, stream,
+          (_ex(experts), _ex(shared), px, pxs, pf, pe, shape, po, pk, ws.nbytes))
 
 
 def moe_get_error(ws, stream=None) -> int:
