@@ -118,27 +118,37 @@ struct WaitCtl {
   int* err;
   unsigned long long limit_ns;
 };
-// Bounded wait; false if it gave up (or another role already did).
+// Bounded wait of a whole warp; false if it gave up (or another role already
+// did).  Every lane asks, so the code around it stays warp-uniform.
 template <bool CLUSTER = false>
 __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const WaitCtl& c, int where) {
-  auto try_once = [&] { return CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity); };
+  auto try_once = [&] {
+    return __all_sync(kFull, CLUSTER ? bar_try_cluster(bar, parity) : bar_try(bar, parity)) != 0;
+  };
   if (try_once()) return true;
   const unsigned long long t0 = global_ns();
   while (!try_once()) {
-    if (*c.abort_flag) return false;
-    if (global_ns() - t0 > c.limit_ns) {
+    if (__any_sync(kFull, *c.abort_flag != 0)) return false;
+    if (__any_sync(kFull, global_ns() - t0 > c.limit_ns)) {
       *c.abort_flag = 1;
-      latch_error(c.err, MOE_ERR_TIMEOUT, where);
+      if ((threadIdx.x & 31) == 0) latch_error(c.err, MOE_ERR_TIMEOUT, where);
       return false;
     }
   }
   return true;
 }
-// The same for a whole warp: lane 0 waits, every lane gets the outcome.
-__device__ __forceinline__ bool bar_wait_warp(uint32_t bar, uint32_t parity, const WaitCtl& c, int where) {
-  int ok = 0;
-  if ((threadIdx.x & 31) == 0) ok = bar_wait(bar, parity, c, where);
-  return __shfl_sync(kFull, ok, 0) != 0;
+// One lane of a converged warp.  Loops that issue copies or MMAs run on the
+// whole warp and only the instruction itself stands under this predicate: the
+// compiler then keeps descriptors and coordinates in uniform registers (under
+// `lane == 0` four MMAs took about 490 clocks to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar,
                                        uint64_t policy) {

@@ -20,6 +20,7 @@
 //   warp 9     TMEM allocation, MMA issue
 //   warp 10    TMA of the activation rows: gathered four at a time by the
 //              bucket's entries, or boxes of consecutive rows
+//   warp 11    the scales of each K block, through shared memory
 // Only rows that exist are fetched.  Small buckets take MR = 16: the stage
 // keeps 2 KB of activations and the MMA's other 112 rows read whatever lies
 // behind (rows of a product do not mix, and nobody reads theirs).
@@ -47,24 +48,32 @@ struct Cfg {
   static constexpr int A_BYTES = MR * 128;
   static constexpr int B_BYTES = BN * 128;
   static constexpr int CP = BN / 2;                  // accumulator columns per thread
-  static constexpr int CH = CP >= 64 ? 32 : SWIGLU || CP == 8 ? (SWIGLU ? CP / 2 : CP) : CP < 32 ? CP : 32;  // columns per TMEM load
+  // columns per TMEM load: two loads' registers beside the accumulators
+  static constexpr int CH = CP == 128 ? 16 : CP == 64 ? 32 : SWIGLU ? CP / 2 : CP;
   static constexpr int BUFS = BN == 256 ? 2 : BN == 128 ? 4 : 8;  // TMEM accumulators
   static constexpr int TMEM = BN * BUFS < 32 ? 32 : BN * BUFS;
   static constexpr int XCH_BYTES = SWIGLU ? 2 * 2 * S * MR * 4 : 0;  // [2][2 S][MR] maxima
   static constexpr int STG_PITCH = 20;               // floats per row of a warp's store tile
   static constexpr int STG_BYTES = kEpiWarps * 32 * STG_PITCH * 4;
-  static constexpr int BUDGET = 227 * 1024 - 8 * 1025 - 1024 - 1024 - XCH_BYTES - STG_BYTES;
-  static constexpr int FIT = BUDGET / (A_BYTES + B_BYTES);
-  static constexpr int NS = FIT > 32 ? 32 : FIT;
+  static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
+  static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 12 * 1024) / (A_BYTES + B_BYTES);
+  static constexpr int NS = BN == 256 && MR == 128 ? 4 : FIT > 24 ? 24 : FIT;
+  // Scale slots: the rows' scales and the two weight scales of a K block.  The
+  // scale warp fills block g's slot once the MMAs of block g - NS are done, so
+  // the epilogue is past block g - NS - BUFS.
+  static constexpr int SLOTS = NS + BUFS;
+  static constexpr int SLOT = MR + 4;                // floats
   // the activation stages come first: an MR = 16 operand overruns into the
   // weight stages, never out of them
   static constexpr int W0 = NS * A_BYTES;
   static constexpr int STG = NS * (A_BYTES + B_BYTES);
   static constexpr int XCH = STG + STG_BYTES;
-  static constexpr int CTL = XCH + XCH_BYTES;        // barriers and flags: 1 KB
-  static constexpr int TAB = CTL + 1024;             // int [2][E + 1]: tiles and rows before e
+  static constexpr int SCL = XCH + XCH_BYTES;
+  static constexpr int CTL = SCL + SLOTS * SLOT * 4; // barriers and flags
+  static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 2) * 8 + 4 * (2 + kThreads / 32) + 15) / 16 * 16;
+  static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
   static constexpr int KREG = BN == 256 ? 216 : 0;   // registers of a promoting thread
-  static_assert(NS >= 4 && NS * B_BYTES >= 128 * 128, "stages");
+  static_assert(NS >= 4 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT, "shared memory");
   static size_t smem(int E) { return size_t(TAB) + 8 * size_t(E + 1) + 1024 /*alignment*/; }
 };
 
@@ -153,26 +162,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + C::NS;
   uint64_t* acc_full = empty + C::NS;          // [BUFS]
   uint64_t* acc_empty = acc_full + C::BUFS;    // [BUFS]
-  uint64_t* drain = acc_empty + C::BUFS;
+  uint64_t* scl_full = acc_empty + C::BUFS;    // [SLOTS]
+  uint64_t* drain = scl_full + C::SLOTS;
   uint64_t* xbar = drain + 1;                  // row maxima of the cluster are in place
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* xch = reinterpret_cast<float*>(smem + C::XCH);
+  float* scl = reinterpret_cast<float*>(smem + C::SCL);
   int* s_part = const_cast<int*>(abort_flag) + 1;  // [warps]
   int* t_off = reinterpret_cast<int*>(smem + C::TAB);
   int* t_beg = t_off + (a.E + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(kFull, int(threadIdx.x) >> 5, 0), lane = threadIdx.x & 31;
   const int rank = S > 1 ? int(cluster_rank()) : 0;
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::NS; ++s) {
-      bar_init(smem_addr(&full[s]), 2);  // the weights' and the rows' producer
+      bar_init(smem_addr(&full[s]), 3);  // the weights', the rows' and the scales' producer
       bar_init(smem_addr(&empty[s]), 1);
     }
     for (int b = 0; b < C::BUFS; ++b) {
       bar_init(smem_addr(&acc_full[b]), 1);
       bar_init(smem_addr(&acc_empty[b]), kEpiWarps);
     }
+    for (int s = 0; s < C::SLOTS; ++s) bar_init(smem_addr(&scl_full[s]), 1);
     bar_init(smem_addr(drain), 1);
     bar_init(smem_addr(xbar), kEpiWarps * S);
     *abort_flag = 0;
@@ -253,40 +265,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kEpiWarps) {
       // ------------------------------------------------------ weight producer
-      if (lane == 0) {
-        Ring<C::NS> ring;
-        uint32_t fills = 0, used = 0;
-        uint64_t keep, once;
-        asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
-        asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
-        bool ok = true;
-        for (int it = first; it < n_tiles && ok; it += step) {
-          const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
-          // weights that one row tile alone reads are not worth keeping in L2
-          const uint64_t pol = t_beg[t.e + 1] - t_beg[t.e] <= MR ? once : keep;
-          const int wrow = t.e * a.N + t.nt * C::COLS + rank * C::WBOX;
-          for (int kb = 0; kb < KB; ++kb, ring.next()) {
-            ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 510);
-            if (!ok) break;
-            const uint32_t w = smem_addr(smem + C::W0 + ring.stage * C::B_BYTES);
-            const uint32_t fb = smem_addr(&full[ring.stage]);
-            // debug switch: the first stage gets no weights, so the MMA
-            // thread's bounded wait on it runs out
-            if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kb == 0) continue;
+      Ring<C::NS> ring;
+      uint32_t fills = 0, used = 0;
+      uint64_t keep, once;
+      asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
+      bool ok = true;
+      for (int it = first; it < n_tiles && ok; it += step) {
+        const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
+        // weights that one row tile alone reads are not worth keeping in L2
+        const uint64_t pol = t_beg[t.e + 1] - t_beg[t.e] <= MR ? once : keep;
+        const int wrow = t.e * a.N + t.nt * C::COLS + rank * C::WBOX;
+        for (int kb = 0; kb < KB; ++kb, ring.next()) {
+          ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 510);
+          if (!ok) break;
+          const uint32_t w = smem_addr(smem + C::W0 + ring.stage * C::B_BYTES);
+          const uint32_t fb = smem_addr(&full[ring.stage]);
+          // debug switch: the first stage gets no weights, so the MMA warp's
+          // bounded wait on it runs out
+          if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kb == 0) continue;
+          if (elect_one()) {
             bar_expect(fb, C::B_BYTES);
             tma_2d(w, &maps.w[0], kb * 128, wrow, fb, pol);
             if (SWIGLU) tma_2d(w + C::WBOX * 128, &maps.w[1], kb * 128, wrow, fb, pol);
-            fills ^= 1u << ring.stage;
-            used |= 1u << ring.stage;
           }
+          fills ^= 1u << ring.stage;
+          used |= 1u << ring.stage;
         }
-        // after a give-up, let every copy that was requested land (bounded)
-        if (*abort_flag) {
-          for (int s = 0; s < C::NS; ++s) {
-            if (!((used >> s) & 1u)) continue;
-            const unsigned long long t0 = global_ns();
-            while (!bar_try(smem_addr(&full[s]), ((fills >> s) & 1u) ^ 1u) && global_ns() - t0 < 100000000ull) {
-            }
+      }
+      // after a give-up, let every copy that was requested land (bounded)
+      if (*abort_flag && lane == 0) {
+        for (int s = 0; s < C::NS; ++s) {
+          if (!((used >> s) & 1u)) continue;
+          const unsigned long long t0 = global_ns();
+          while (!bar_try(smem_addr(&full[s]), ((fills >> s) & 1u) ^ 1u) && global_ns() - t0 < 100000000ull) {
           }
         }
       }
@@ -313,42 +325,107 @@ __global__ void __launch_bounds__(kThreads, 1)
           bytes = (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
         }
         for (int kb = 0; kb < KB; ++kb, ring.next()) {
-          ok = bar_wait_warp(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 511);
+          ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 511);
           if (!ok) break;
           const uint32_t st = smem_addr(smem + ring.stage * C::A_BYTES), fb = smem_addr(&full[ring.stage]);
-          if (lane == 0) bar_expect(fb, bytes);
+          if (elect_one()) bar_expect(fb, bytes);
           __syncwarp();
           if (gather) {
             if (4 * lane < t.nvalid) tma_gather4(st + lane * 512, &maps.a, kb * 128, r[0], r[1], r[2], r[3], fb);
-          } else if (C::ABOX * lane < t.nvalid) {
-            tma_2d(st + lane * C::ABOX * 128, &maps.a, kb * 128, t.row0 + C::ABOX * lane, fb, keep);
+          } else if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < MR / C::ABOX; ++j)
+              if (C::ABOX * j < t.nvalid)
+                tma_2d(st + j * C::ABOX * 128, &maps.a, kb * 128, t.row0 + C::ABOX * j, fb, keep);
+          }
+          __syncwarp();
+        }
+      }
+    } else if (warp == kEpiWarps + 3) {
+      // ------------------------------------------------------- scale producer
+      // lane l holds rows l, l + 32, ..; lanes 0 and 1 the two weight scales
+      // (the column halves' blocks, or gate and up).  UK K blocks a round,
+      // so that their loads are in flight together.
+      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 4 : 2;
+      Ring<C::NS> ring;
+      Ring<C::SLOTS> slot;
+      const int NB = fp8_blocks(a.N);
+      bool ok = true;
+      for (int it = first; it < n_tiles && ok; it += step) {
+        const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
+        const float* sa[RJ];
+#pragma unroll
+        for (int j = 0; j < RJ; ++j) {
+          int src = t.row0 + min(lane + 32 * j, t.nvalid - 1);
+          if (gather) src = a.entries[src] / a.a_div;
+          sa[j] = a.a_s + size_t(src >= 0 && src < a.a_rows ? src : 0) * KB;
+        }
+        const int h = lane & 1;
+        const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * C::CP) / kFp8Block, NB - 1);
+        const float* sw = a.w_s[SWIGLU ? h : 0] + (size_t(t.e) * NB + nb) * KB;
+        for (int kb = 0; kb < KB && ok; kb += UK) {
+          float va[UK][RJ], vw[UK];
+#pragma unroll
+          for (int u = 0; u < UK; ++u) {
+            const int k = min(kb + u, KB - 1);
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) va[u][j] = sa[j][k];
+            vw[u] = sw[k];
+          }
+#pragma unroll
+          for (int u = 0; u < UK; ++u) {
+            if (kb + u >= KB) break;
+            ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 512);
+            if (!ok) break;
+            float* to = scl + slot.stage * C::SLOT;
+#pragma unroll
+            for (int j = 0; j < RJ; ++j)
+              if (MR >= 32 || lane < MR) to[lane + 32 * j] = va[u][j];
+            if (lane < 2) to[MR + lane] = vw[u];
+            __syncwarp();
+            if (lane == 0) {
+              bar_arrive(smem_addr(&scl_full[slot.stage]));
+              // the MMAs wait for this warp too: it must not fall a round of
+              // the ring behind, where the empty barrier's parity repeats
+              bar_arrive(smem_addr(&full[ring.stage]));
+            }
+            ring.next();
+            slot.next();
           }
         }
       }
-    } else if (warp == kEpiWarps + 1 && lane == 0) {
+    } else if (warp == kEpiWarps + 1) {
       // ----------------------------------------------------------------- MMA
       Ring<C::NS> ring;
       Ring<C::BUFS> acc;
       bool ok = true;
       constexpr uint32_t idesc = idesc_e4m3(MR == 16 ? 64 : 128, BN);
+      const uint64_t da0 = desc_k_sw128(smem_addr(smem)), dw0 = desc_k_sw128(smem_addr(smem + C::W0));
       for (int it = first; it < n_tiles && ok; it += step) {
         for (int kb = 0; kb < KB; ++kb, ring.next(), acc.next()) {
           ok = bar_wait(smem_addr(&acc_empty[acc.stage]), acc.phase ^ 1u, ctl, 520) &&
                bar_wait(smem_addr(&full[ring.stage]), ring.phase, ctl, 521);
           if (!ok) break;
           tcgen_fence_after();
-          const uint32_t sa = smem_addr(smem + ring.stage * C::A_BYTES);
-          const uint32_t sw = smem_addr(smem + C::W0 + ring.stage * C::B_BYTES);
-          const int steps = min(4, (a.K - kb * 128 + 31) / 32);  // the tail reads zero fill
-          for (int k = 0; k < steps; ++k)
-            mma_e4m3(tmem + acc.stage * BN, desc_k_sw128(sa + 32 * k), desc_k_sw128(sw + 32 * k), idesc, k != 0);
-          tcgen_commit(smem_addr(&empty[ring.stage]));
-          tcgen_commit(smem_addr(&acc_full[acc.stage]));
+          // descriptors count addresses in units of 16 bytes
+          const uint64_t da = da0 + uint32_t(ring.stage * (C::A_BYTES / 16));
+          const uint64_t dw = dw0 + uint32_t(ring.stage * (C::B_BYTES / 16));
+          const uint32_t d = tmem + acc.stage * BN;
+          const int left = a.K - kb * 128;  // a tail of K reads zero fill to its next 32
+          if (elect_one()) {
+            mma_e4m3(d, da, dw, idesc, 0);
+            if (left > 32) mma_e4m3(d, da + 2, dw + 2, idesc, 1);
+            if (left > 64) mma_e4m3(d, da + 4, dw + 4, idesc, 1);
+            if (left > 96) mma_e4m3(d, da + 6, dw + 6, idesc, 1);
+            tcgen_commit(smem_addr(&empty[ring.stage]));
+            tcgen_commit(smem_addr(&acc_full[acc.stage]));
+          }
+          __syncwarp();
         }
       }
       if (!ok || *abort_flag) {
         // let issued MMAs finish before TMEM is released (bounded)
-        tcgen_commit(smem_addr(drain));
+        if (elect_one()) tcgen_commit(smem_addr(drain));
         const unsigned long long t0 = global_ns();
         while (!bar_try(smem_addr(drain), 0) && global_ns() - t0 < 200000000ull) {
         }
@@ -362,6 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int NB = fp8_blocks(a.N);
     float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
     Ring<C::BUFS> acc;
+    Ring<C::SLOTS> slot;
     uint32_t local = 0;  // tiles so far
     bool ok = true;
     for (int it = first; it < n_tiles && ok; it += step, ++local) {
@@ -380,28 +458,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           src = dst = 0;
         }
       }
-      // this thread's row scales and its columns' weight block
       const int n0 = SWIGLU ? t.nt * 128 + rank * C::WBOX + half * (BN / 4) : t.nt * BN + half * C::CP;
-      const int nb = min(n0 / kFp8Block, NB - 1);
-      const float* sa = a.a_s + size_t(src) * KB;
-      const float* sw0 = a.w_s[0] + (size_t(t.e) * NB + nb) * KB;
-      const float* sw1 = SWIGLU ? a.w_s[1] + (size_t(t.e) * NB + nb) * KB : sw0;
       const bool work = 32 * q < t.nvalid;  // this warp's rows exist
       float2 v[C::CP / 2];
 #pragma unroll
       for (int j = 0; j < C::CP / 2; ++j) v[j] = make_float2(0.f, 0.f);
-      float na = sa[0], nw0 = sw0[0], nw1 = SWIGLU ? sw1[0] : 0.f;
-      for (int kb = 0; kb < KB; ++kb, acc.next()) {
-        const float s0 = na * nw0, s1 = SWIGLU ? na * nw1 : 0.f;
-        if (kb + 1 < KB) {
-          na = sa[kb + 1];
-          nw0 = sw0[kb + 1];
-          if (SWIGLU) nw1 = sw1[kb + 1];
-        }
-        if (!bar_wait_warp(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530)) {
-          ok = false;
-          break;
-        }
+      for (int kb = 0; kb < KB; ++kb, acc.next(), slot.next()) {
+        ok = bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531);
+        if (!ok) break;
+        const float* sc = scl + slot.stage * C::SLOT;
+        const float s_row = sc[MR >= 128 ? row : row & (MR - 1)];
+        const float s0 = s_row * sc[MR + (SWIGLU ? 0 : half)], s1 = SWIGLU ? s_row * sc[MR + 1] : 0.f;
+        ok = bar_wait(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530);
+        if (!ok) break;
         if (work) {
           tcgen_fence_after();
           const uint32_t col = tmem + acc.stage * BN + (uint32_t(32 * q) << 16);
@@ -455,9 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (S > 1) cluster_arrive(cluster_map(smem_addr(xbar), lane));
           else bar_arrive(smem_addr(xbar));
         }
-        int got = 0;
-        if (lane == 0) got = bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540);
-        ok = __shfl_sync(kFull, got, 0) != 0;
+        ok = bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540);
         if (!ok) break;
         if (row < MR) {
 #pragma unroll
