@@ -49,11 +49,11 @@ struct Cfg {
   static constexpr int B_BYTES = BN * 128;
   static constexpr int CP = BN / 2;                  // accumulator columns per thread
   // columns per TMEM load: two loads' registers beside the accumulators
-  static constexpr int CH = CP == 128 ? 16 : CP == 64 ? 32 : SWIGLU ? CP / 2 : CP;
+  static constexpr int CH = CP >= 64 ? 32 : SWIGLU ? CP / 2 : CP;
   static constexpr int BUFS = BN == 256 ? 2 : BN == 128 ? 4 : 8;  // TMEM accumulators
   static constexpr int TMEM = BN * BUFS < 32 ? 32 : BN * BUFS;
   static constexpr int XCH_BYTES = SWIGLU ? 2 * 2 * S * MR * 4 : 0;  // [2][2 S][MR] maxima
-  static constexpr int STG_PITCH = 20;               // floats per row of a warp's store tile
+  static constexpr int STG_PITCH = 20;               // floats per row of a warp's store tile: 16, 4 spare
   static constexpr int STG_BYTES = kEpiWarps * 32 * STG_PITCH * 4;
   static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
   static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 12 * 1024) / (A_BYTES + B_BYTES);
@@ -261,6 +261,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool gather = a.a_div > 0;
   const WaitCtl ctl{abort_flag, a.err, wait_us ? wait_us * 1000ull : kLimitNs};
 
+  // the end of every role.  (Each side of the register split calls it by itself
+  // and returns: where the two meet again, ptxas holds both to the launch's
+  // registers and the accumulators spill.)
+  auto finish = [&] {
+    __syncwarp();
+    tcgen_fence_before();
+    if (S > 1) cluster_barrier();  // no CTA leaves while another may write its maxima
+    else __syncthreads();
+    if (warp == kEpiWarps + 1) {
+      tcgen_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM)
+                   : "memory");
+    }
+  };
+
   if (warp >= kEpiWarps) {
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kEpiWarps) {
@@ -431,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    finish();
   } else {
     // --------------------------------------------------- promotion, epilogue
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::KREG));
@@ -438,28 +454,32 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int row = 32 * q + lane;
     const int NB = fp8_blocks(a.N);
     float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
+    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH + 16);
     Ring<C::BUFS> acc;
     Ring<C::SLOTS> slot;
     uint32_t local = 0;  // tiles so far
     bool ok = true;
     for (int it = first; it < n_tiles && ok; it += step, ++local) {
-      const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
-      const bool in = row < t.nvalid;
-      const int p = t.row0 + min(row, t.nvalid - 1);
-      int src = p, dst = p;
-      bool good = in;
-      if (gather || a.scatter) {
-        const int ent = a.entries[p];
-        if (gather) src = ent / a.a_div;
-        if (a.scatter) dst = ent;
-        if (ent < 0 || src >= a.a_rows || dst >= a.P) {
-          if (in) latch_error(a.err, MOE_ERR_DEVICE_DATA, 501);
-          good = false;
-          src = dst = 0;
+      // what the tile's end needs waits beside this lane's row of the store tile:
+      // the registers are the accumulators'
+      bool work;  // this warp's rows exist
+      {
+        const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
+        work = 32 * q < t.nvalid;
+        int src = t.row0 + min(row, t.nvalid - 1), dst = src;
+        bool good = row < t.nvalid;
+        if (gather || a.scatter) {
+          const int ent = a.entries[src];
+          if (gather) src = ent / a.a_div;
+          if (a.scatter) dst = ent;
+          if (ent < 0 || src >= a.a_rows || dst >= a.P) {
+            if (good) latch_error(a.err, MOE_ERR_DEVICE_DATA, 501);
+            good = false;
+          }
         }
+        park[0] = good ? dst : -1;
+        park[1] = t.nt;
       }
-      const int n0 = SWIGLU ? t.nt * 128 + rank * C::WBOX + half * (BN / 4) : t.nt * BN + half * C::CP;
-      const bool work = 32 * q < t.nvalid;  // this warp's rows exist
       float2 v[C::CP / 2];
 #pragma unroll
       for (int j = 0; j < C::CP / 2; ++j) v[j] = make_float2(0.f, 0.f);
@@ -480,16 +500,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int o = c * CH;
             return SWIGLU ? (o < BN / 4 ? 0 : BN / 4) + half * (BN / 4) + o : half * C::CP + o;
           };
-          uint32_t d[2][CH];
-          tmem_load<CH>(col + at(0), d[0]);
+          uint32_t d[CH];
 #pragma unroll
           for (int c = 0; c < NCH; ++c) {
-            tmem_wait<CH>(d[c & 1]);
-            if (c + 1 < NCH) tmem_load<CH>(col + at(c + 1), d[(c + 1) & 1]);
+            tmem_load<CH>(col + at(c), d);
+            tmem_wait<CH>(d);
             const float s = SWIGLU && c * CH >= BN / 4 ? s1 : s0;
 #pragma unroll
             for (int j = 0; j < CH / 2; ++j)
-              fma_pair(v[c * CH / 2 + j], d[c & 1][2 * j], d[c & 1][2 * j + 1], make_float2(s, s));
+              fma_pair(v[c * CH / 2 + j], d[2 * j], d[2 * j + 1], make_float2(s, s));
           }
           tcgen_fence_before();
         }
@@ -497,6 +516,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) bar_arrive(smem_addr(&acc_empty[acc.stage]));
       }
       if (!ok) break;
+      const int dst = park[0], nt = park[1];  // output row, negative: none
+      const int n0 = SWIGLU ? nt * 128 + rank * C::WBOX + half * (BN / 4) : nt * BN + half * C::CP;
       if constexpr (SWIGLU) {
         // h in place of the gate values, and its largest magnitude over the
         // block's 128 columns (2 halves x S CTAs).  Two exchange buffers: who
@@ -535,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < HC / 4; ++j)
           w[j] = f32x4_to_e4m3x4(v[2 * j].x * inv, v[2 * j].y * inv, v[2 * j + 1].x * inv, v[2 * j + 1].y * inv);
-        if (good && half == 0 && rank == 0) a.s_out[size_t(p) * NB + t.nt] = s;
+        if (dst >= 0 && half == 0 && rank == 0) a.s_out[size_t(dst) * NB + nt] = s;
         if (!work) continue;
         if constexpr (HC >= 32) {
           // through shared memory: HC / 16 lanes store one row's codes
@@ -548,13 +569,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < LPR; ++i) {
             const int r = i * (32 / LPR) + lane / LPR, j = lane % LPR;
-            const bool g = __shfl_sync(kFull, int(good), r) != 0;
-            if (g && n0 + 16 * j < a.N)  // N is a multiple of 16
-              *reinterpret_cast<uint4*>(a.q_out + size_t(t.row0 + 32 * q + r) * a.N + n0 + 16 * j) = st4[r * 5 + j];
+            const int drow = __shfl_sync(kFull, dst, r);
+            if (drow >= 0 && n0 + 16 * j < a.N)  // N is a multiple of 16
+              *reinterpret_cast<uint4*>(a.q_out + size_t(drow) * a.N + n0 + 16 * j) = st4[r * 5 + j];
           }
           __syncwarp();
-        } else if (good && n0 < a.N) {
-          uint8_t* o = a.q_out + size_t(p) * a.N + n0;
+        } else if (dst >= 0 && n0 < a.N) {
+          uint8_t* o = a.q_out + size_t(dst) * a.N + n0;
           if constexpr (HC == 16) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
           else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
         }
@@ -563,7 +584,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // of one row instead of 32 rows' single words
         constexpr int PC = C::CP < 16 ? C::CP : 16;
         const bool vec = a.N % 4 == 0;
-        const unsigned rows_ok = __ballot_sync(kFull, good);
 #pragma unroll
         for (int c = 0; c < C::CP / PC; ++c) {
           const int n = n0 + c * PC, left = a.N - n;
@@ -580,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < LPR; ++i) {
               const int r = i * (32 / LPR) + lane / LPR, j = 4 * (lane % LPR);
               const int drow = __shfl_sync(kFull, dst, r);
-              if (((rows_ok >> r) & 1u) && j < left) {
+              if (drow >= 0 && j < left) {
                 const float4 f = *reinterpret_cast<const float4*>(stg + r * C::STG_PITCH + j);
                 const size_t o = size_t(drow) * a.N + n + j;
                 if (a.out_type == MOE_DTYPE_F32)
@@ -595,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < PC; ++i) {
               const int r = i * (32 / PC) + lane / PC, j = lane % PC;
               const int drow = __shfl_sync(kFull, dst, r);
-              if (((rows_ok >> r) & 1u) && j < left)
+              if (drow >= 0 && j < left)
                 store_one(a.out, a.out_type, size_t(drow) * a.N + n + j, stg[r * C::STG_PITCH + j]);
             }
           }
@@ -603,16 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  }
-
-  __syncwarp();
-  tcgen_fence_before();
-  if (S > 1) cluster_barrier();  // no CTA leaves while another may write its maxima
-  else __syncthreads();
-  if (warp == kEpiWarps + 1) {
-    tcgen_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM)
-                 : "memory");
+    finish();
   }
 }
 

@@ -204,6 +204,26 @@ def test_gemm(rows, N, K, dt):
     assert (out[rows:] == 7.0).all()  # the row behind the last is left alone
 
 
+def test_gemm_many_tiles_per_sm():
+    """Several tiles on every SM with a short K: the rings wrap within tiles and
+    across them."""
+    rng = np.random.default_rng(12)
+    rows, N, K = 2100, 9000, 656
+    aq, as_ = rows8(rng, rows, K)
+    wq, ws_ = mats8(rng, 1, N, K)
+    ws = make_ws()
+    moe.moe_workspace_set_limits(ws, 100000)
+    out = torch.empty(rows, N, device="cuda")
+    args = [dev(t) for t in (aq, as_, wq[0], ws_[0])]
+    for _ in range(4):
+        moe.moe_gemm_fp8(*args, out, ws)
+    assert moe.moe_get_error(ws) == 0
+    a, w = F.dequant_rows(aq, as_), F.dequant_mats(wq[0], ws_[0])
+    pick = rng.permutation(rows)[:200]
+    want, mag = F.gemm(a[pick], w)
+    check_prod(out[dev(pick)], want, mag, K, F32)
+
+
 def test_gemm_block_scales_and_order():
     """One-hot operands: every (row, column, K) position meets its own scales."""
     N, K, rows = 384, 512, 4
