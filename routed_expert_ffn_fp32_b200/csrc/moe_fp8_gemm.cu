@@ -30,6 +30,9 @@
 // be joined.  The fused pair needs the largest |h| of each 128 columns: its
 // narrow tiles form a cluster of 2, 4 or 8 CTAs that share such a block and
 // exchange each row's maximum through distributed shared memory.
+#include <atomic>
+#include <type_traits>
+
 #include "moe_fp8.cuh"
 
 namespace moe {
@@ -45,13 +48,19 @@ struct Cfg {
   static constexpr int COLS = SWIGLU ? 128 : BN;     // output columns per tile (of the cluster)
   static constexpr int WBOX = SWIGLU ? BN / 2 : BN;  // weight rows per copy
   static constexpr int ABOX = MR < 32 ? MR : 32;     // activation rows per copy
-  static constexpr int A_BYTES = MR * 128;
-  static constexpr int B_BYTES = BN * 128;
+  // K blocks per stage: narrow tiles take several, their barriers cost more
+  // than their MMAs
+  static constexpr int KU = BN == 256 || (BN == 128 && MR == 128) ? 1 : BN == 128 || MR == 128 ? 2 : 4;
+  static constexpr int A_BLK = MR * 128, B_BLK = BN * 128;
+  static constexpr int A_BYTES = KU * A_BLK, B_BYTES = KU * B_BLK;  // per stage
   static constexpr int CP = BN / 2;                  // accumulator columns per thread
   // columns per TMEM load: two loads' registers beside the accumulators
   static constexpr int CH = CP >= 64 ? 32 : SWIGLU ? CP / 2 : CP;
-  static constexpr int BUFS = BN == 256 ? 2 : BN == 128 ? 4 : 8;  // TMEM accumulators
-  static constexpr int TMEM = BN * BUFS < 32 ? 32 : BN * BUFS;
+  static constexpr int UB = KU * CH > 64 ? 64 / CH : KU;  // K blocks per round of TMEM loads
+  // TMEM accumulator sets, one accumulator per K block of a stage
+  static constexpr int BUFS = BN * KU >= 256 ? 2 : 4;
+  static constexpr int TMEM = BN * KU * BUFS;
+  static constexpr int PROMOTERS = MR == 16 ? 2 : kEpiWarps;
   static constexpr int XCH_BYTES = SWIGLU ? 2 * 2 * S * MR * 4 : 0;  // [2][2 S][MR] maxima
   static constexpr int STG_PITCH = 20;               // floats per row of a warp's store tile: 16, 4 spare
   static constexpr int STG_BYTES = kEpiWarps * 32 * STG_PITCH * 4;
@@ -62,18 +71,19 @@ struct Cfg {
   // scale warp fills block g's slot once the MMAs of block g - NS are done, so
   // the epilogue is past block g - NS - BUFS.
   static constexpr int SLOTS = NS + BUFS;
-  static constexpr int SLOT = MR + 4;                // floats
+  static constexpr int SLOT = MR + 4;                // floats, per K block
   // the activation stages come first: an MR = 16 operand overruns into the
   // weight stages, never out of them
   static constexpr int W0 = NS * A_BYTES;
   static constexpr int STG = NS * (A_BYTES + B_BYTES);
   static constexpr int XCH = STG + STG_BYTES;
   static constexpr int SCL = XCH + XCH_BYTES;
-  static constexpr int CTL = SCL + SLOTS * SLOT * 4; // barriers and flags
-  static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 2) * 8 + 4 * (2 + kThreads / 32) + 15) / 16 * 16;
+  static constexpr int CTL = SCL + SLOTS * KU * SLOT * 4; // barriers and flags
+  static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + kThreads / 32) + 15) / 16 * 16;
   static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
   static constexpr int KREG = BN == 256 ? 216 : 0;   // registers of a promoting thread
-  static_assert(NS >= 4 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT, "shared memory");
+  static_assert(NS >= 3 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT && TMEM <= 512, "shared memory, TMEM");
+  static_assert(MR != 16 || 16 * (BN + 4) * 4 <= STG_BYTES, "tile buffer");
   static size_t smem(int E) { return size_t(TAB) + 8 * size_t(E + 1) + 1024 /*alignment*/; }
 };
 
@@ -137,6 +147,52 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
+// W consecutive values of one row
+template <typename T, int W>
+__device__ __forceinline__ void store_word(T* o, const float* f) {
+  constexpr int type = sizeof(T) == 4 ? MOE_DTYPE_F32 : std::is_same_v<T, __half> ? MOE_DTYPE_F16 : MOE_DTYPE_BF16;
+  if constexpr (W == 1) store_one(o, type, 0, f[0]);
+  else if constexpr (sizeof(T) == 4 && W == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(f);
+  else if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(f);
+  else if constexpr (W == 4)
+    *reinterpret_cast<uint2*>(o) = make_uint2(pack16(type, f[0], f[1]), pack16(type, f[2], f[3]));
+  else *reinterpret_cast<uint32_t*>(o) = pack16(type, f[0], f[1]);
+}
+
+// A warp's 32 rows x CP columns (lane l: row l in v, its output row dst or -1)
+// to out [.., N] from column n0 on.  They pass through the warp's store tile 16
+// columns at a time, so that each store covers runs of a few rows instead of
+// one word in each of 32.
+template <typename T, int W, int CP>
+__device__ __forceinline__ void store_tile(T* out, int N, int n0, const float2 (&v)[CP / 2], float* stg, int dst) {
+  constexpr int PITCH = 20, PC = CP < 16 ? CP : 16, LPR = PC / W, RPI = 32 / LPR;  // lanes per row, rows per store
+  const int lane = threadIdx.x & 31, j = W * (lane % LPR);
+  int drow[LPR];
+#pragma unroll
+  for (int i = 0; i < LPR; ++i) drow[i] = __shfl_sync(kFull, dst, i * RPI + lane / LPR);
+#pragma unroll
+  for (int c = 0; c < CP / PC; ++c) {
+    const int n = n0 + c * PC + j;
+    if (n0 + c * PC >= N) break;
+#pragma unroll
+    for (int k = 0; k < PC / 4; ++k)
+      *reinterpret_cast<float4*>(stg + lane * PITCH + 4 * k) =
+          make_float4(v[c * PC / 2 + 2 * k].x, v[c * PC / 2 + 2 * k].y, v[c * PC / 2 + 2 * k + 1].x,
+                      v[c * PC / 2 + 2 * k + 1].y);
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < LPR; ++i)
+      if (drow[i] >= 0 && n < N)
+        store_word<T, W>(out + size_t(drow[i]) * N + n, stg + (i * RPI + lane / LPR) * PITCH + j);
+    __syncwarp();
+  }
+}
+
 // A stage ring's position.
 template <int NS>
 struct Ring {
@@ -165,7 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* scl_full = acc_empty + C::BUFS;    // [SLOTS]
   uint64_t* drain = scl_full + C::SLOTS;
   uint64_t* xbar = drain + 1;                  // row maxima of the cluster are in place
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
+  uint64_t* stg_full = xbar + 1;               // MR = 16: a tile's sums are in shared memory
+  uint64_t* stg_empty = stg_full + 1;          // and have been stored
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stg_empty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float* xch = reinterpret_cast<float*>(smem + C::XCH);
   float* scl = reinterpret_cast<float*>(smem + C::SCL);
@@ -182,11 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < C::BUFS; ++b) {
       bar_init(smem_addr(&acc_full[b]), 1);
-      bar_init(smem_addr(&acc_empty[b]), kEpiWarps);
+      bar_init(smem_addr(&acc_empty[b]), C::PROMOTERS);
     }
     for (int s = 0; s < C::SLOTS; ++s) bar_init(smem_addr(&scl_full[s]), 1);
     bar_init(smem_addr(drain), 1);
-    bar_init(smem_addr(xbar), kEpiWarps * S);
+    bar_init(smem_addr(xbar), (MR == 16 ? kEpiWarps - 2 : kEpiWarps) * S);
+    bar_init(smem_addr(stg_full), 2);
+    bar_init(smem_addr(stg_empty), kEpiWarps - 2);
     *abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(&maps.a) : "memory");
@@ -256,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   else __syncthreads();
   const uint32_t tmem = *tmem_slot;
   const int n_tiles = t_off[a.E];
-  const int KB = fp8_blocks(a.K);
+  const int KB = fp8_blocks(a.K), KG = (KB + C::KU - 1) / C::KU;  // K blocks, stages of them
   const int first = blockIdx.x / S, step = gridDim.x / S;
   const bool gather = a.a_div > 0;
   const WaitCtl ctl{abort_flag, a.err, wait_us ? wait_us * 1000ull : kLimitNs};
@@ -291,18 +351,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // weights that one row tile alone reads are not worth keeping in L2
         const uint64_t pol = t_beg[t.e + 1] - t_beg[t.e] <= MR ? once : keep;
         const int wrow = t.e * a.N + t.nt * C::COLS + rank * C::WBOX;
-        for (int kb = 0; kb < KB; ++kb, ring.next()) {
+        for (int kg = 0; kg < KG; ++kg, ring.next()) {
           ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 510);
           if (!ok) break;
           const uint32_t w = smem_addr(smem + C::W0 + ring.stage * C::B_BYTES);
           const uint32_t fb = smem_addr(&full[ring.stage]);
           // debug switch: the first stage gets no weights, so the MMA warp's
           // bounded wait on it runs out
-          if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kb == 0) continue;
+          if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kg == 0) continue;
           if (elect_one()) {
-            bar_expect(fb, C::B_BYTES);
-            tma_2d(w, &maps.w[0], kb * 128, wrow, fb, pol);
-            if (SWIGLU) tma_2d(w + C::WBOX * 128, &maps.w[1], kb * 128, wrow, fb, pol);
+            const int kn = min(C::KU, KB - kg * C::KU);
+            bar_expect(fb, kn * C::B_BLK);
+#pragma unroll
+            for (int u = 0; u < C::KU; ++u) {
+              if (u >= kn) break;
+              const int x = (kg * C::KU + u) * 128;
+              tma_2d(w + u * C::B_BLK, &maps.w[0], x, wrow, fb, pol);
+              if (SWIGLU) tma_2d(w + u * C::B_BLK + C::WBOX * 128, &maps.w[1], x, wrow, fb, pol);
+            }
           }
           fills ^= 1u << ring.stage;
           used |= 1u << ring.stage;
@@ -339,19 +405,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         } else {
           bytes = (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
         }
-        for (int kb = 0; kb < KB; ++kb, ring.next()) {
+        for (int kg = 0; kg < KG; ++kg, ring.next()) {
           ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 511);
           if (!ok) break;
           const uint32_t st = smem_addr(smem + ring.stage * C::A_BYTES), fb = smem_addr(&full[ring.stage]);
-          if (elect_one()) bar_expect(fb, bytes);
+          const int kn = min(C::KU, KB - kg * C::KU);
+          if (elect_one()) bar_expect(fb, kn * bytes);
           __syncwarp();
-          if (gather) {
-            if (4 * lane < t.nvalid) tma_gather4(st + lane * 512, &maps.a, kb * 128, r[0], r[1], r[2], r[3], fb);
-          } else if (elect_one()) {
 #pragma unroll
-            for (int j = 0; j < MR / C::ABOX; ++j)
-              if (C::ABOX * j < t.nvalid)
-                tma_2d(st + j * C::ABOX * 128, &maps.a, kb * 128, t.row0 + C::ABOX * j, fb, keep);
+          for (int u = 0; u < C::KU; ++u) {
+            if (u >= kn) break;
+            const int x = (kg * C::KU + u) * 128;
+            const uint32_t to = st + u * C::A_BLK;
+            if (gather) {
+              if (4 * lane < t.nvalid) tma_gather4(to + lane * 512, &maps.a, x, r[0], r[1], r[2], r[3], fb);
+            } else if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < MR / C::ABOX; ++j)
+                if (C::ABOX * j < t.nvalid)
+                  tma_2d(to + j * C::ABOX * 128, &maps.a, x, t.row0 + C::ABOX * j, fb, keep);
+            }
           }
           __syncwarp();
         }
@@ -361,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // lane l holds rows l, l + 32, ..; lanes 0 and 1 the two weight scales
       // (the column halves' blocks, or gate and up).  UK K blocks a round,
       // so that their loads are in flight together.
-      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 4 : 2;
+      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 4 : 2, UG = UK / C::KU;
       Ring<C::NS> ring;
       Ring<C::SLOTS> slot;
       const int NB = fp8_blocks(a.N);
@@ -378,25 +451,28 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int h = lane & 1;
         const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * C::CP) / kFp8Block, NB - 1);
         const float* sw = a.w_s[SWIGLU ? h : 0] + (size_t(t.e) * NB + nb) * KB;
-        for (int kb = 0; kb < KB && ok; kb += UK) {
+        for (int kg = 0; kg < KG && ok; kg += UG) {
           float va[UK][RJ], vw[UK];
 #pragma unroll
           for (int u = 0; u < UK; ++u) {
-            const int k = min(kb + u, KB - 1);
+            const int k = min(kg * C::KU + u, KB - 1);
 #pragma unroll
             for (int j = 0; j < RJ; ++j) va[u][j] = sa[j][k];
             vw[u] = sw[k];
           }
 #pragma unroll
-          for (int u = 0; u < UK; ++u) {
-            if (kb + u >= KB) break;
+          for (int g = 0; g < UG; ++g) {
+            if (kg + g >= KG) break;
             ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 512);
             if (!ok) break;
-            float* to = scl + slot.stage * C::SLOT;
 #pragma unroll
-            for (int j = 0; j < RJ; ++j)
-              if (MR >= 32 || lane < MR) to[lane + 32 * j] = va[u][j];
-            if (lane < 2) to[MR + lane] = vw[u];
+            for (int u = 0; u < C::KU; ++u) {
+              float* to = scl + (slot.stage * C::KU + u) * C::SLOT;
+#pragma unroll
+              for (int j = 0; j < RJ; ++j)
+                if (MR >= 32 || lane < MR) to[lane + 32 * j] = va[g * C::KU + u][j];
+              if (lane < 2) to[MR + lane] = vw[g * C::KU + u];
+            }
             __syncwarp();
             if (lane == 0) {
               bar_arrive(smem_addr(&scl_full[slot.stage]));
@@ -417,21 +493,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr uint32_t idesc = idesc_e4m3(MR == 16 ? 64 : 128, BN);
       const uint64_t da0 = desc_k_sw128(smem_addr(smem)), dw0 = desc_k_sw128(smem_addr(smem + C::W0));
       for (int it = first; it < n_tiles && ok; it += step) {
-        for (int kb = 0; kb < KB; ++kb, ring.next(), acc.next()) {
+        for (int kg = 0; kg < KG; ++kg, ring.next(), acc.next()) {
           ok = bar_wait(smem_addr(&acc_empty[acc.stage]), acc.phase ^ 1u, ctl, 520) &&
                bar_wait(smem_addr(&full[ring.stage]), ring.phase, ctl, 521);
           if (!ok) break;
           tcgen_fence_after();
-          // descriptors count addresses in units of 16 bytes
-          const uint64_t da = da0 + uint32_t(ring.stage * (C::A_BYTES / 16));
-          const uint64_t dw = dw0 + uint32_t(ring.stage * (C::B_BYTES / 16));
-          const uint32_t d = tmem + acc.stage * BN;
-          const int left = a.K - kb * 128;  // a tail of K reads zero fill to its next 32
+          const int left = a.K - kg * C::KU * 128;  // a tail of K reads zero fill to its next 32
           if (elect_one()) {
-            mma_e4m3(d, da, dw, idesc, 0);
-            if (left > 32) mma_e4m3(d, da + 2, dw + 2, idesc, 1);
-            if (left > 64) mma_e4m3(d, da + 4, dw + 4, idesc, 1);
-            if (left > 96) mma_e4m3(d, da + 6, dw + 6, idesc, 1);
+#pragma unroll
+            for (int u = 0; u < C::KU; ++u) {
+              // descriptors count addresses in units of 16 bytes
+              const uint64_t da = da0 + uint32_t((ring.stage * C::A_BYTES + u * C::A_BLK) / 16);
+              const uint64_t dw = dw0 + uint32_t((ring.stage * C::B_BYTES + u * C::B_BLK) / 16);
+              const uint32_t d = tmem + (acc.stage * C::KU + u) * BN;
+              if (left > u * 128) mma_e4m3(d, da, dw, idesc, 0);
+              if (left > u * 128 + 32) mma_e4m3(d, da + 2, dw + 2, idesc, 1);
+              if (left > u * 128 + 64) mma_e4m3(d, da + 4, dw + 4, idesc, 1);
+              if (left > u * 128 + 96) mma_e4m3(d, da + 6, dw + 6, idesc, 1);
+            }
             tcgen_commit(smem_addr(&empty[ring.stage]));
             tcgen_commit(smem_addr(&acc_full[acc.stage]));
           }
@@ -453,69 +532,197 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int q = warp & 3, half = warp >> 2;
     const int row = 32 * q + lane;
     const int NB = fp8_blocks(a.N);
-    float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
-    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH + 16);
     Ring<C::BUFS> acc;
     Ring<C::SLOTS> slot;
     uint32_t local = 0;  // tiles so far
     bool ok = true;
-    for (int it = first; it < n_tiles && ok; it += step, ++local) {
-      // what the tile's end needs waits beside this lane's row of the store tile:
-      // the registers are the accumulators'
-      bool work;  // this warp's rows exist
-      {
-        const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
-        work = 32 * q < t.nvalid;
-        int src = t.row0 + min(row, t.nvalid - 1), dst = src;
-        bool good = row < t.nvalid;
-        if (gather || a.scatter) {
-          const int ent = a.entries[src];
-          if (gather) src = ent / a.a_div;
-          if (a.scatter) dst = ent;
-          if (ent < 0 || src >= a.a_rows || dst >= a.P) {
-            if (good) latch_error(a.err, MOE_ERR_DEVICE_DATA, 501);
-            good = false;
-          }
-        }
-        park[0] = good ? dst : -1;
-        park[1] = t.nt;
-      }
-      float2 v[C::CP / 2];
+    // column of this half's value o (swiglu: its gate, then its up columns)
+    auto at = [&](int o) {
+      return SWIGLU ? (o < BN / 4 ? 0 : BN / 4) + half * (BN / 4) + o : half * C::CP + o;
+    };
+    // the sums of one tile over K; work: this warp's rows exist
+    auto promote = [&](float2 (&v)[C::CP / 2], bool work) {
 #pragma unroll
       for (int j = 0; j < C::CP / 2; ++j) v[j] = make_float2(0.f, 0.f);
-      for (int kb = 0; kb < KB; ++kb, acc.next(), slot.next()) {
-        ok = bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531);
-        if (!ok) break;
-        const float* sc = scl + slot.stage * C::SLOT;
-        const float s_row = sc[MR >= 128 ? row : row & (MR - 1)];
-        const float s0 = s_row * sc[MR + (SWIGLU ? 0 : half)], s1 = SWIGLU ? s_row * sc[MR + 1] : 0.f;
-        ok = bar_wait(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530);
-        if (!ok) break;
+      for (int kg = 0; kg < KG; ++kg, acc.next(), slot.next()) {
+        if (!bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531)) return false;
+        const float* sc = scl + slot.stage * C::KU * C::SLOT;
+        float s0[C::KU], s1[C::KU];
+#pragma unroll
+        for (int u = 0; u < C::KU; ++u) {
+          const float s_row = sc[u * C::SLOT + (MR >= 128 ? row : row & (MR - 1))];
+          s0[u] = s_row * sc[u * C::SLOT + MR + (SWIGLU ? 0 : half)];
+          s1[u] = SWIGLU ? s_row * sc[u * C::SLOT + MR + 1] : 0.f;
+        }
+        const int kn = min(C::KU, KB - kg * C::KU);
+        if (!bar_wait(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530)) return false;
         if (work) {
           tcgen_fence_after();
-          const uint32_t col = tmem + acc.stage * BN + (uint32_t(32 * q) << 16);
-          // columns of chunk c: of this half (swiglu: its gate, then its up columns)
-          constexpr int CH = C::CH, NCH = C::CP / CH;
-          auto at = [&](int c) {
-            const int o = c * CH;
-            return SWIGLU ? (o < BN / 4 ? 0 : BN / 4) + half * (BN / 4) + o : half * C::CP + o;
-          };
-          uint32_t d[CH];
+          const uint32_t col = tmem + acc.stage * C::KU * BN + (uint32_t(32 * q) << 16);
+          constexpr int CH = C::CH, UB = C::UB;
 #pragma unroll
-          for (int c = 0; c < NCH; ++c) {
-            tmem_load<CH>(col + at(c), d);
-            tmem_wait<CH>(d);
-            const float s = SWIGLU && c * CH >= BN / 4 ? s1 : s0;
+          for (int c = 0; c < C::CP / CH; ++c) {
 #pragma unroll
-            for (int j = 0; j < CH / 2; ++j)
-              fma_pair(v[c * CH / 2 + j], d[2 * j], d[2 * j + 1], make_float2(s, s));
+            for (int u0 = 0; u0 < C::KU; u0 += UB) {
+              // a short last stage reads an old accumulator and leaves it out
+              uint32_t d[UB][CH];
+#pragma unroll
+              for (int u = 0; u < UB; ++u) tmem_load<CH>(col + (u0 + u) * BN + at(c * CH), d[u]);
+#pragma unroll
+              for (int u = 0; u < UB; ++u) {
+                tmem_wait<CH>(d[u]);
+                if (u0 + u >= kn) break;
+                const float s = SWIGLU && c * CH >= BN / 4 ? s1[u0 + u] : s0[u0 + u];
+#pragma unroll
+                for (int j = 0; j < CH / 2; ++j)
+                  fma_pair(v[c * CH / 2 + j], d[u][2 * j], d[u][2 * j + 1], make_float2(s, s));
+              }
+            }
           }
           tcgen_fence_before();
         }
         __syncwarp();
         if (lane == 0) bar_arrive(smem_addr(&acc_empty[acc.stage]));
       }
-      if (!ok) break;
+      return true;
+    };
+    // output row of bucket position p, or -1 (latched) for an entry that names
+    // no row
+    auto out_row = [&](int p) {
+      if (!gather && !a.scatter) return p;
+      const int ent = a.entries[p];
+      if (ent < 0 || (gather && ent / a.a_div >= a.a_rows) || (a.scatter && ent >= a.P)) {
+        latch_error(a.err, MOE_ERR_DEVICE_DATA, 501);
+        return -1;
+      }
+      return a.scatter ? ent : p;
+    };
+    if constexpr (MR == 16) {
+      // Only TMEM quarter 0 holds rows: its two warps promote, leave the tile in
+      // shared memory and go on; the other six store it meanwhile.
+      constexpr int PITCH = BN + 4;
+      float* buf = reinterpret_cast<float*>(smem + C::STG);
+      if (q == 0) {
+        for (int it = first; it < n_tiles; it += step, ++local) {
+          float2 v[C::CP / 2];
+          if (!promote(v, true) || !bar_wait(smem_addr(stg_empty), (local & 1u) ^ 1u, ctl, 541)) break;
+          if (lane < 16) {
+#pragma unroll
+            for (int j = 0; j < C::CP / 4; ++j)
+              *reinterpret_cast<float4*>(buf + lane * PITCH + at(4 * j)) =
+                  make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(stg_full));
+        }
+      } else {
+        const int hw = warp - (half ? 2 : 1);  // 0 .. 5
+        for (int it = first; it < n_tiles; it += step, ++local) {
+          const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
+          const int dst = lane < t.nvalid ? out_row(t.row0 + lane) : -1;  // of row `lane`
+          if (!bar_wait(smem_addr(stg_full), local & 1u, ctl, 542)) break;
+          if constexpr (SWIGLU) {
+            // a warp per row, up to three of them; CPL columns per lane
+            constexpr int HC = BN / 2, CPL = HC < 32 ? 1 : HC / 32, HR = 3;
+            const int c = lane * CPL, n = t.nt * 128 + rank * HC + c;
+            float h[HR][CPL], amax[HR];
+#pragma unroll
+            for (int i = 0; i < HR; ++i) {
+              const int r = hw + 6 * i;
+              amax[i] = 0.f;
+#pragma unroll
+              for (int j = 0; j < CPL; ++j) {
+                h[i][j] = 0.f;
+                if (r < t.nvalid && c < HC && n + j < a.N)
+                  h[i][j] = silu_mul(buf[r * PITCH + c + j], buf[r * PITCH + HC + c + j]);
+                amax[i] = fmaxf(amax[i], fabsf(h[i][j]));
+              }
+#pragma unroll
+              for (int o = 16; o > 0; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(kFull, amax[i], o));
+            }
+            if constexpr (S > 1) {
+              // the block's other columns are in the cluster's other CTAs.  Two
+              // exchange buffers: who writes one again has seen everyone arrive
+              // for the other, and they arrive after their reads.
+              float* x = xch + (local & 1u) * (S * MR);
+              if (lane < S) {
+#pragma unroll
+                for (int i = 0; i < HR; ++i)
+                  if (hw + 6 * i < t.nvalid)
+                    cluster_st(cluster_map(smem_addr(x + rank * MR + hw + 6 * i), lane), amax[i]);
+                cluster_arrive(cluster_map(smem_addr(xbar), lane));
+              }
+              __syncwarp();
+              if (!bar_wait<true>(smem_addr(xbar), local & 1u, ctl, 540)) break;
+#pragma unroll
+              for (int i = 0; i < HR; ++i)
+                if (hw + 6 * i < t.nvalid)
+#pragma unroll
+                  for (int k = 0; k < S; ++k) amax[i] = fmaxf(amax[i], x[k * MR + hw + 6 * i]);
+            }
+#pragma unroll
+            for (int i = 0; i < HR; ++i) {
+              const int r = hw + 6 * i;
+              if (r >= t.nvalid) break;
+              const int drow = __shfl_sync(kFull, dst, r);
+              if (drow < 0) continue;
+              const float s = fp8_scale(amax[i]), inv = 1.f / s;
+              if (lane == 0 && rank == 0) a.s_out[size_t(drow) * NB + t.nt] = s;
+              if (c < HC && n < a.N) {  // N is a multiple of 16
+                uint8_t* o = a.q_out + size_t(drow) * a.N + n;
+                if constexpr (CPL == 4)
+                  *reinterpret_cast<uint32_t*>(o) =
+                      f32x4_to_e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
+                else if constexpr (CPL == 2)
+                  *reinterpret_cast<uint16_t*>(o) = uint16_t(f32x2_to_e4m3x2(h[i][0] * inv, h[i][1] * inv));
+                else
+                  *o = uint8_t(f32x2_to_e4m3x2(h[i][0] * inv, 0.f));
+              }
+            }
+          } else {
+            // four columns of a row per lane, all rows' quads in turn
+            constexpr int QUADS = BN / 4;
+            const bool vec = a.N % 4 == 0;
+            for (int b = hw * 32; b < t.nvalid * QUADS; b += 6 * 32) {
+              const int r = (b + lane) / QUADS, j = 4 * ((b + lane) % QUADS);
+              const int drow = __shfl_sync(kFull, dst, r & 15), left = a.N - t.nt * BN - j;
+              if (r >= t.nvalid || drow < 0 || left <= 0) continue;
+              const float4 f = *reinterpret_cast<const float4*>(buf + r * PITCH + j);
+              const size_t o = size_t(drow) * a.N + t.nt * BN + j;
+              if (!vec) {
+                store_one(a.out, a.out_type, o, f.x);
+                if (left > 1) store_one(a.out, a.out_type, o + 1, f.y);
+                if (left > 2) store_one(a.out, a.out_type, o + 2, f.z);
+                if (left > 3) store_one(a.out, a.out_type, o + 3, f.w);
+              } else if (a.out_type == MOE_DTYPE_F32) {
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = f;
+              } else {
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
+                    make_uint2(pack16(a.out_type, f.x, f.y), pack16(a.out_type, f.z, f.w));
+              }
+            }
+          }
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(stg_empty));
+        }
+      }
+      finish();
+      return;
+    }
+    float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
+    // what the tile's end needs waits beside this lane's row of the store tile:
+    // the registers are the accumulators'
+    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH + 16);
+    for (int it = first; it < n_tiles; it += step, ++local) {
+      bool work;
+      {
+        const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
+        work = 32 * q < t.nvalid;
+        park[0] = row < t.nvalid ? out_row(t.row0 + row) : -1;
+        park[1] = t.nt;
+      }
+      float2 v[C::CP / 2];
+      if (!promote(v, work)) break;
       const int dst = park[0], nt = park[1];  // output row, negative: none
       const int n0 = SWIGLU ? nt * 128 + rank * C::WBOX + half * (BN / 4) : nt * BN + half * C::CP;
       if constexpr (SWIGLU) {
@@ -580,47 +787,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
         }
       } else if (work) {
-        // through shared memory, PC columns a pass, so that a warp stores runs
-        // of one row instead of 32 rows' single words
-        constexpr int PC = C::CP < 16 ? C::CP : 16;
-        const bool vec = a.N % 4 == 0;
-#pragma unroll
-        for (int c = 0; c < C::CP / PC; ++c) {
-          const int n = n0 + c * PC, left = a.N - n;
-          if (left <= 0) break;
-#pragma unroll
-          for (int j = 0; j < PC / 4; ++j)
-            *reinterpret_cast<float4*>(stg + lane * C::STG_PITCH + 4 * j) =
-                make_float4(v[c * PC / 2 + 2 * j].x, v[c * PC / 2 + 2 * j].y, v[c * PC / 2 + 2 * j + 1].x,
-                            v[c * PC / 2 + 2 * j + 1].y);
-          __syncwarp();
-          if (vec) {
-            constexpr int LPR = PC / 4;  // lanes per row, four columns each
-#pragma unroll
-            for (int i = 0; i < LPR; ++i) {
-              const int r = i * (32 / LPR) + lane / LPR, j = 4 * (lane % LPR);
-              const int drow = __shfl_sync(kFull, dst, r);
-              if (drow >= 0 && j < left) {
-                const float4 f = *reinterpret_cast<const float4*>(stg + r * C::STG_PITCH + j);
-                const size_t o = size_t(drow) * a.N + n + j;
-                if (a.out_type == MOE_DTYPE_F32)
-                  *reinterpret_cast<float4*>(static_cast<float*>(a.out) + o) = f;
-                else
-                  *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + o) =
-                      make_uint2(pack16(a.out_type, f.x, f.y), pack16(a.out_type, f.z, f.w));
-              }
-            }
-          } else {
-#pragma unroll
-            for (int i = 0; i < PC; ++i) {
-              const int r = i * (32 / PC) + lane / PC, j = lane % PC;
-              const int drow = __shfl_sync(kFull, dst, r);
-              if (drow >= 0 && j < left)
-                store_one(a.out, a.out_type, size_t(drow) * a.N + n + j, stg[r * C::STG_PITCH + j]);
-            }
-          }
-          __syncwarp();
-        }
+        const int word = a.N % 4 == 0 ? 4 : a.N % 2 == 0 ? 2 : 1;  // columns that stay aligned in every row
+        auto put = [&](auto type, auto w) {
+          store_tile<decltype(type), decltype(w)::value, C::CP>(static_cast<decltype(type)*>(a.out), a.N, n0, v, stg, dst);
+        };
+        auto by_word = [&](auto type) {
+          if (word == 4) put(type, Int<4>{});
+          else if (word == 2) put(type, Int<2>{});
+          else put(type, Int<1>{});
+        };
+        if (a.out_type == MOE_DTYPE_F32) by_word(float{});
+        else if (a.out_type == MOE_DTYPE_BF16) by_word(__nv_bfloat16{});
+        else by_word(__half{});
       }
     }
     finish();
@@ -640,8 +818,17 @@ cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   if (SWIGLU && !make_tma_map_u8_box(&m.w[1], a.w_q[1], a.K, wrows, 128, C::WBOX)) return cudaErrorInvalidValue;
   auto kern = k_gemm_fp8<SWIGLU, BN, MR>;
   const size_t smem = C::smem(a.E);
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  // the kernel's shared-memory limit, set once per device
+  static std::atomic<unsigned long long> set{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (dev >= 64 || !(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::smem(kMaxExperts)));
+    if (e != cudaSuccess) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t cfg = {};
   const long long most = device_info().sm_count / C::S;
   cfg.gridDim = dim3(unsigned((max_tiles < most ? max_tiles : most) * C::S));
