@@ -38,8 +38,6 @@
 namespace moe {
 namespace {
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 384;
 constexpr unsigned long long kLimitNs = 2000000000ull;  // default bound of a wait: 2 s
 
 template <bool SWIGLU, int BN, int MR>
@@ -53,19 +51,24 @@ struct Cfg {
   static constexpr int KU = BN == 256 || (BN == 128 && MR == 128) ? 1 : BN == 128 || MR == 128 ? 2 : 4;
   static constexpr int A_BLK = MR * 128, B_BLK = BN * 128;
   static constexpr int A_BYTES = KU * A_BLK, B_BYTES = KU * B_BLK;  // per stage
-  static constexpr int CP = BN / 2;                  // accumulator columns per thread
+  static constexpr int EW = 8;                       // promoting warps: 4 TMEM quarters x PARTS column parts
+  static constexpr int PARTS = EW / 4;
+  static constexpr int THREADS = (EW + 4) * 32;
+  static constexpr int CP = BN / PARTS;              // accumulator columns per thread
   // columns per TMEM load: two loads' registers beside the accumulators
-  static constexpr int CH = CP >= 64 ? 32 : SWIGLU ? CP / 2 : CP;
+  static constexpr int CH = CP == 128 ? 16 : CP == 64 ? 32 : SWIGLU ? CP / 2 : CP;
   static constexpr int UB = KU * CH > 64 ? 64 / CH : KU;  // K blocks per round of TMEM loads
   // TMEM accumulator sets, one accumulator per K block of a stage
   static constexpr int BUFS = BN * KU >= 256 ? 2 : 4;
   static constexpr int TMEM = BN * KU * BUFS;
-  static constexpr int PROMOTERS = MR == 16 ? 2 : kEpiWarps;
-  static constexpr int XCH_BYTES = SWIGLU ? 2 * 2 * S * MR * 4 : 0;  // [2][2 S][MR] maxima
-  static constexpr int STG_PITCH = 20;               // floats per row of a warp's store tile: 16, 4 spare
-  static constexpr int STG_BYTES = kEpiWarps * 32 * STG_PITCH * 4;
+  static constexpr int PROMOTERS = MR == 16 ? 2 : EW;
+  static constexpr int XCH_BYTES = SWIGLU ? 2 * PARTS * S * MR * 4 : 0;  // [2][PARTS S][MR] maxima
+  // MR = 16: a tile's sums.  Otherwise per lane 8 values on their way out, the
+  // lane's output row and the tile's column block, and padding.
+  static constexpr int STG_PITCH = SWIGLU ? 2 : 11;
+  static constexpr int STG_BYTES = MR == 16 ? 16 * (BN + 4) * 4 : EW * 32 * STG_PITCH * 4;
   static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
-  static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 12 * 1024) / (A_BYTES + B_BYTES);
+  static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 14 * 1024) / (A_BYTES + B_BYTES);
   static constexpr int NS = BN == 256 && MR == 128 ? 4 : FIT > 24 ? 24 : FIT;
   // Scale slots: the rows' scales and the two weight scales of a K block.  The
   // scale warp fills block g's slot once the MMAs of block g - NS are done, so
@@ -79,11 +82,11 @@ struct Cfg {
   static constexpr int XCH = STG + STG_BYTES;
   static constexpr int SCL = XCH + XCH_BYTES;
   static constexpr int CTL = SCL + SLOTS * KU * SLOT * 4; // barriers and flags
-  static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + kThreads / 32) + 15) / 16 * 16;
+  static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + THREADS / 32) + 15) / 16 * 16;
   static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
-  static constexpr int KREG = BN == 256 ? 216 : 0;   // registers of a promoting thread
+  // registers of a promoting thread, and of the others (0: all the same)
+  static constexpr int KREG = BN == 256 ? 208 : 0, KREG_LESS = 88;
   static_assert(NS >= 3 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT && TMEM <= 512, "shared memory, TMEM");
-  static_assert(MR != 16 || 16 * (BN + 4) * 4 <= STG_BYTES, "tile buffer");
   static size_t smem(int E) { return size_t(TAB) + 8 * size_t(E + 1) + 1024 /*alignment*/; }
 };
 
@@ -147,48 +150,68 @@ __device__ __forceinline__ uint32_t pack16(int type, float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-template <int V>
-struct Int {
-  static constexpr int value = V;
-};
+__device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+               "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
 
-// W consecutive values of one row
-template <typename T, int W>
-__device__ __forceinline__ void store_word(T* o, const float* f) {
-  constexpr int type = sizeof(T) == 4 ? MOE_DTYPE_F32 : std::is_same_v<T, __half> ? MOE_DTYPE_F16 : MOE_DTYPE_BF16;
-  if constexpr (W == 1) store_one(o, type, 0, f[0]);
-  else if constexpr (sizeof(T) == 4 && W == 4) *reinterpret_cast<float4*>(o) = *reinterpret_cast<const float4*>(f);
-  else if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(o) = *reinterpret_cast<const float2*>(f);
-  else if constexpr (W == 4)
-    *reinterpret_cast<uint2*>(o) = make_uint2(pack16(type, f[0], f[1]), pack16(type, f[2], f[3]));
-  else *reinterpret_cast<uint32_t*>(o) = pack16(type, f[0], f[1]);
+// CP values of one row from column n0 on, 32 bytes a store; n0 and N are
+// multiples of the values in 32 bytes.
+template <int CP, typename T>
+__device__ __forceinline__ void store_sectors(T* out, int N, int n0, const float2 (&v)[CP / 2], int dst) {
+  constexpr int E = 32 / sizeof(T);
+  T* o = out + size_t(dst) * N + n0;
+#pragma unroll
+  for (int c = 0; c < CP / E; ++c) {
+    if (n0 + c * E >= N) break;
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if constexpr (sizeof(T) == 4) w[k] = __float_as_uint(k & 1 ? v[c * 4 + k / 2].y : v[c * 4 + k / 2].x);
+      else w[k] = pack16(std::is_same_v<T, __half> ? MOE_DTYPE_F16 : MOE_DTYPE_BF16, v[c * 8 + k].x, v[c * 8 + k].y);
+    }
+    st_sector(o + c * E, w);
+  }
 }
 
 // A warp's 32 rows x CP columns (lane l: row l in v, its output row dst or -1)
-// to out [.., N] from column n0 on.  They pass through the warp's store tile 16
-// columns at a time, so that each store covers runs of a few rows instead of
-// one word in each of 32.
-template <typename T, int W, int CP>
-__device__ __forceinline__ void store_tile(T* out, int N, int n0, const float2 (&v)[CP / 2], float* stg, int dst) {
-  constexpr int PITCH = 20, PC = CP < 16 ? CP : 16, LPR = PC / W, RPI = 32 / LPR;  // lanes per row, rows per store
-  const int lane = threadIdx.x & 31, j = W * (lane % LPR);
-  int drow[LPR];
-#pragma unroll
-  for (int i = 0; i < LPR; ++i) drow[i] = __shfl_sync(kFull, dst, i * RPI + lane / LPR);
+// to rows of any width N.  They pass through shared memory 8 columns at a time,
+// so that a store covers runs of several rows' neighbours instead of one word
+// in each of 32; word: columns a lane stores at once (4, 2 or 1, N a multiple).
+template <int CP>
+__device__ __forceinline__ void store_tile(void* out, int type, int word, int N, int n0, const float2 (&v)[CP / 2],
+                                           float* stg, int dst) {
+  constexpr int PITCH = 11, PC = 8;
+  const int lane = threadIdx.x & 31;
+  const int lpr = PC / word, rpi = 32 / lpr;  // lanes per row, rows per store
+  const int j = word * (lane % lpr), r0 = lane / lpr;
 #pragma unroll
   for (int c = 0; c < CP / PC; ++c) {
-    const int n = n0 + c * PC + j;
     if (n0 + c * PC >= N) break;
 #pragma unroll
-    for (int k = 0; k < PC / 4; ++k)
-      *reinterpret_cast<float4*>(stg + lane * PITCH + 4 * k) =
-          make_float4(v[c * PC / 2 + 2 * k].x, v[c * PC / 2 + 2 * k].y, v[c * PC / 2 + 2 * k + 1].x,
-                      v[c * PC / 2 + 2 * k + 1].y);
+    for (int k = 0; k < PC; ++k) stg[lane * PITCH + k] = k & 1 ? v[(c * PC + k) / 2].y : v[(c * PC + k) / 2].x;
     __syncwarp();
-#pragma unroll
-    for (int i = 0; i < LPR; ++i)
-      if (drow[i] >= 0 && n < N)
-        store_word<T, W>(out + size_t(drow[i]) * N + n, stg + (i * RPI + lane / LPR) * PITCH + j);
+    const int n = n0 + c * PC + j;
+#pragma unroll 1
+    for (int i = 0; i < lpr; ++i) {
+      const int r = i * rpi + r0;
+      const int drow = __shfl_sync(kFull, dst, r);
+      if (drow < 0 || n >= N) continue;
+      const float* f = stg + r * PITCH + j;
+      const size_t o = size_t(drow) * N + n;
+      if (word == 1) {
+        store_one(out, type, o, f[0]);
+      } else if (type == MOE_DTYPE_F32) {
+        float* d = static_cast<float*>(out) + o;
+        if (word == 4) *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
+        else *reinterpret_cast<float2*>(d) = make_float2(f[0], f[1]);
+      } else {
+        uint16_t* d = static_cast<uint16_t*>(out) + o;
+        if (word == 4) *reinterpret_cast<uint2*>(d) = make_uint2(pack16(type, f[0], f[1]), pack16(type, f[2], f[3]));
+        else *reinterpret_cast<uint32_t*>(d) = pack16(type, f[0], f[1]);
+      }
+    }
     __syncwarp();
   }
 }
@@ -207,10 +230,10 @@ struct Ring {
 };
 
 template <bool SWIGLU, int BN, int MR>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
     k_gemm_fp8(const __grid_constant__ Fp8GemmArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<SWIGLU, BN, MR>;
-  constexpr int S = C::S;
+  constexpr int S = C::S, kEpiWarps = C::EW, kThreads = C::THREADS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -337,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   if (warp >= kEpiWarps) {
-    if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::KREG_LESS));
     if (warp == kEpiWarps) {
       // ------------------------------------------------------ weight producer
       Ring<C::NS> ring;
@@ -432,9 +455,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
       // lane l holds rows l, l + 32, ..; lanes 0 and 1 the two weight scales
-      // (the column halves' blocks, or gate and up).  UK K blocks a round,
-      // so that their loads are in flight together.
-      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 4 : 2, UG = UK / C::KU;
+      // (the column halves' blocks, or gate and up).  UK K blocks a round, and
+      // the next round's loads in flight: their latency is several stages'.
+      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 8 : 4, UG = UK / C::KU;
       Ring<C::NS> ring;
       Ring<C::SLOTS> slot;
       const int NB = fp8_blocks(a.N);
@@ -449,17 +472,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           sa[j] = a.a_s + size_t(src >= 0 && src < a.a_rows ? src : 0) * KB;
         }
         const int h = lane & 1;
-        const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * C::CP) / kFp8Block, NB - 1);
+        const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * (BN / 2)) / kFp8Block, NB - 1);
         const float* sw = a.w_s[SWIGLU ? h : 0] + (size_t(t.e) * NB + nb) * KB;
-        for (int kg = 0; kg < KG && ok; kg += UG) {
-          float va[UK][RJ], vw[UK];
+        float next_a[UK][RJ], next_w[UK];
+        auto load = [&](int kg) {
 #pragma unroll
           for (int u = 0; u < UK; ++u) {
             const int k = min(kg * C::KU + u, KB - 1);
 #pragma unroll
-            for (int j = 0; j < RJ; ++j) va[u][j] = sa[j][k];
-            vw[u] = sw[k];
+            for (int j = 0; j < RJ; ++j) next_a[u][j] = sa[j][k];
+            next_w[u] = sw[k];
           }
+        };
+        load(0);
+        for (int kg = 0; kg < KG && ok; kg += UG) {
+          float va[UK][RJ], vw[UK];
+#pragma unroll
+          for (int u = 0; u < UK; ++u) {
+#pragma unroll
+            for (int j = 0; j < RJ; ++j) va[u][j] = next_a[u][j];
+            vw[u] = next_w[u];
+          }
+          if (kg + UG < KG) load(kg + UG);
 #pragma unroll
           for (int g = 0; g < UG; ++g) {
             if (kg + g >= KG) break;
@@ -529,39 +563,52 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // --------------------------------------------------- promotion, epilogue
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::KREG));
-    const int q = warp & 3, half = warp >> 2;
+    const int q = warp & 3, part = warp >> 2;
     const int row = 32 * q + lane;
     const int NB = fp8_blocks(a.N);
     Ring<C::BUFS> acc;
     Ring<C::SLOTS> slot;
     uint32_t local = 0;  // tiles so far
     bool ok = true;
-    // column of this half's value o (swiglu: its gate, then its up columns)
-    auto at = [&](int o) {
-      return SWIGLU ? (o < BN / 4 ? 0 : BN / 4) + half * (BN / 4) + o : half * C::CP + o;
-    };
+    // column of this part's value o (swiglu: its gate, then its up columns)
+    constexpr int HP = C::CP / 2;
+    auto at = [&](int o) { return SWIGLU ? (o < HP ? o : BN / 2 + o - HP) + part * HP : part * C::CP + o; };
     // the sums of one tile over K; work: this warp's rows exist
     auto promote = [&](float2 (&v)[C::CP / 2], bool work) {
 #pragma unroll
       for (int j = 0; j < C::CP / 2; ++j) v[j] = make_float2(0.f, 0.f);
-      for (int kg = 0; kg < KG; ++kg, acc.next(), slot.next()) {
+      float s0[C::KU], s1[C::KU];
+      auto scales = [&] {  // of the next stage in turn
         if (!bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531)) return false;
         const float* sc = scl + slot.stage * C::KU * C::SLOT;
-        float s0[C::KU], s1[C::KU];
 #pragma unroll
         for (int u = 0; u < C::KU; ++u) {
           const float s_row = sc[u * C::SLOT + (MR >= 128 ? row : row & (MR - 1))];
-          s0[u] = s_row * sc[u * C::SLOT + MR + (SWIGLU ? 0 : half)];
+          s0[u] = s_row * sc[u * C::SLOT + MR + (SWIGLU ? 0 : part / (C::PARTS / 2))];
           s1[u] = SWIGLU ? s_row * sc[u * C::SLOT + MR + 1] : 0.f;
         }
+        slot.next();
+        return true;
+      };
+      // (small buckets read the scales a stage ahead; the full tile has no
+      // registers left for that)
+      constexpr bool AHEAD = MR == 16;
+      if (AHEAD && !scales()) return false;
+      for (int kg = 0; kg < KG; ++kg, acc.next()) {
         const int kn = min(C::KU, KB - kg * C::KU);
+        if (!AHEAD && !scales()) return false;
         if (!bar_wait(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530)) return false;
+        auto release = [&] {  // the MMAs may have the buffer
+          tcgen_fence_before();
+          __syncwarp();
+          if (lane == 0) bar_arrive(smem_addr(&acc_empty[acc.stage]));
+        };
         if (work) {
           tcgen_fence_after();
           const uint32_t col = tmem + acc.stage * C::KU * BN + (uint32_t(32 * q) << 16);
-          constexpr int CH = C::CH, UB = C::UB;
+          constexpr int CH = C::CH, UB = C::UB, NCH = C::CP / CH;
 #pragma unroll
-          for (int c = 0; c < C::CP / CH; ++c) {
+          for (int c = 0; c < NCH; ++c) {
 #pragma unroll
             for (int u0 = 0; u0 < C::KU; u0 += UB) {
               // a short last stage reads an old accumulator and leaves it out
@@ -569,20 +616,22 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int u = 0; u < UB; ++u) tmem_load<CH>(col + (u0 + u) * BN + at(c * CH), d[u]);
 #pragma unroll
+              for (int u = 0; u < UB; ++u) tmem_wait<CH>(d[u]);
+              if (c + 1 == NCH && u0 + UB >= C::KU) release();
+#pragma unroll
               for (int u = 0; u < UB; ++u) {
-                tmem_wait<CH>(d[u]);
                 if (u0 + u >= kn) break;
-                const float s = SWIGLU && c * CH >= BN / 4 ? s1[u0 + u] : s0[u0 + u];
+                const float s = SWIGLU && c * CH >= HP ? s1[u0 + u] : s0[u0 + u];
 #pragma unroll
                 for (int j = 0; j < CH / 2; ++j)
                   fma_pair(v[c * CH / 2 + j], d[u][2 * j], d[u][2 * j + 1], make_float2(s, s));
               }
             }
           }
-          tcgen_fence_before();
+        } else {
+          release();
         }
-        __syncwarp();
-        if (lane == 0) bar_arrive(smem_addr(&acc_empty[acc.stage]));
+        if (AHEAD && kg + 1 < KG && !scales()) return false;
       }
       return true;
     };
@@ -616,7 +665,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) bar_arrive(smem_addr(stg_full));
         }
       } else {
-        const int hw = warp - (half ? 2 : 1);  // 0 .. 5
+        const int hw = warp - (part ? 2 : 1);  // 0 .. 5
         for (int it = first; it < n_tiles; it += step, ++local) {
           const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
           const int dst = lane < t.nvalid ? out_row(t.row0 + lane) : -1;  // of row `lane`
@@ -710,9 +759,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       return;
     }
     float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
-    // what the tile's end needs waits beside this lane's row of the store tile:
-    // the registers are the accumulators'
-    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH + 16);
+    // what the tile's end needs waits in shared memory: the registers are the
+    // accumulators'
+    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH) + (SWIGLU ? 0 : 8);
     for (int it = first; it < n_tiles; it += step, ++local) {
       bool work;
       {
@@ -724,81 +773,68 @@ __global__ void __launch_bounds__(kThreads, 1)
       float2 v[C::CP / 2];
       if (!promote(v, work)) break;
       const int dst = park[0], nt = park[1];  // output row, negative: none
-      const int n0 = SWIGLU ? nt * 128 + rank * C::WBOX + half * (BN / 4) : nt * BN + half * C::CP;
       if constexpr (SWIGLU) {
         // h in place of the gate values, and its largest magnitude over the
-        // block's 128 columns (2 halves x S CTAs).  Two exchange buffers: who
-        // writes one again has seen everyone arrive for the other, and they
-        // arrive after their reads.
-        constexpr int HC = BN / 4;  // h columns per thread
+        // block's 128 columns (PARTS here, in each of S CTAs).  Two exchange
+        // buffers: who writes one again has seen everyone arrive for the other,
+        // and they arrive after their reads.
+        const int n0 = nt * 128 + rank * C::WBOX + part * HP;
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < HC / 2; ++j) {
-          v[j].x = silu_mul(v[j].x, v[HC / 2 + j].x);
-          v[j].y = silu_mul(v[j].y, v[HC / 2 + j].y);
+        for (int j = 0; j < HP / 2; ++j) {
+          v[j].x = silu_mul(v[j].x, v[HP / 2 + j].x);
+          v[j].y = silu_mul(v[j].y, v[HP / 2 + j].y);
           if (n0 + 2 * j < a.N) amax = fmaxf(amax, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
         }
-        const uint32_t x = (local & 1u) * (2 * S * MR);
-        if (row < MR) {
-          const uint32_t mine = smem_addr(xch + x + (2 * rank + half) * MR + row);
+        float* x = xch + (local & 1u) * (C::PARTS * S * MR);
+        float* mine = x + (C::PARTS * rank + part) * MR + row;
+        if constexpr (S > 1) {
 #pragma unroll
-          for (int k = 0; k < S; ++k) {
-            if (S > 1) cluster_st(cluster_map(mine, k), amax);
-            else xch[x + half * MR + row] = amax;
-          }
+          for (int k = 0; k < S; ++k) cluster_st(cluster_map(smem_addr(mine), k), amax);
+        } else {
+          *mine = amax;
         }
         __syncwarp();
         if (lane < S) {
           if (S > 1) cluster_arrive(cluster_map(smem_addr(xbar), lane));
           else bar_arrive(smem_addr(xbar));
         }
-        ok = bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540);
-        if (!ok) break;
-        if (row < MR) {
+        if (!bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540)) break;
 #pragma unroll
-          for (int k = 0; k < 2 * S; ++k) amax = fmaxf(amax, xch[x + k * MR + row]);
-        }
-        const float s = fp8_scale(amax), inv = 1.f / s;
-        uint32_t w[HC / 4];
-#pragma unroll
-        for (int j = 0; j < HC / 4; ++j)
-          w[j] = f32x4_to_e4m3x4(v[2 * j].x * inv, v[2 * j].y * inv, v[2 * j + 1].x * inv, v[2 * j + 1].y * inv);
-        if (dst >= 0 && half == 0 && rank == 0) a.s_out[size_t(dst) * NB + nt] = s;
-        if (!work) continue;
-        if constexpr (HC >= 32) {
-          // through shared memory: HC / 16 lanes store one row's codes
-          uint4* st4 = reinterpret_cast<uint4*>(stg);
-#pragma unroll
-          for (int j = 0; j < HC / 16; ++j)
-            st4[lane * 5 + j] = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-          __syncwarp();
-          constexpr int LPR = HC / 16;  // lanes per row
-#pragma unroll
-          for (int i = 0; i < LPR; ++i) {
-            const int r = i * (32 / LPR) + lane / LPR, j = lane % LPR;
-            const int drow = __shfl_sync(kFull, dst, r);
-            if (drow >= 0 && n0 + 16 * j < a.N)  // N is a multiple of 16
-              *reinterpret_cast<uint4*>(a.q_out + size_t(drow) * a.N + n0 + 16 * j) = st4[r * 5 + j];
-          }
-          __syncwarp();
-        } else if (dst >= 0 && n0 < a.N) {
+        for (int k = 0; k < C::PARTS * S; ++k) amax = fmaxf(amax, x[k * MR + row]);
+        if (dst >= 0 && n0 < a.N) {
+          const float s = fp8_scale(amax), inv = 1.f / s;
+          if (part == 0 && rank == 0) a.s_out[size_t(dst) * NB + nt] = s;
           uint8_t* o = a.q_out + size_t(dst) * a.N + n0;
-          if constexpr (HC == 16) *reinterpret_cast<uint4*>(o) = make_uint4(w[0], w[1], w[2], w[3]);
-          else *reinterpret_cast<uint2*>(o) = make_uint2(w[0], w[1]);
+          auto code4 = [&](int j) {
+            return f32x4_to_e4m3x4(v[2 * j].x * inv, v[2 * j].y * inv, v[2 * j + 1].x * inv, v[2 * j + 1].y * inv);
+          };
+          if constexpr (HP == 8) {
+            *reinterpret_cast<uint2*>(o) = make_uint2(code4(0), code4(1));
+          } else {
+#pragma unroll
+            for (int j = 0; j < HP / 16; ++j)
+              if (n0 + 16 * j < a.N)  // N is a multiple of 16
+                *reinterpret_cast<uint4*>(o + 16 * j) =
+                    make_uint4(code4(4 * j), code4(4 * j + 1), code4(4 * j + 2), code4(4 * j + 3));
+          }
         }
       } else if (work) {
-        const int word = a.N % 4 == 0 ? 4 : a.N % 2 == 0 ? 2 : 1;  // columns that stay aligned in every row
-        auto put = [&](auto type, auto w) {
-          store_tile<decltype(type), decltype(w)::value, C::CP>(static_cast<decltype(type)*>(a.out), a.N, n0, v, stg, dst);
-        };
-        auto by_word = [&](auto type) {
-          if (word == 4) put(type, Int<4>{});
-          else if (word == 2) put(type, Int<2>{});
-          else put(type, Int<1>{});
-        };
-        if (a.out_type == MOE_DTYPE_F32) by_word(float{});
-        else if (a.out_type == MOE_DTYPE_BF16) by_word(__nv_bfloat16{});
-        else by_word(__half{});
+        const int n0 = nt * BN + part * C::CP;
+        // rows of whole sectors: every lane stores its own row, 32 bytes a time
+        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 &&
+                             a.N % (a.out_type == MOE_DTYPE_F32 ? 8 : 16) == 0 &&
+                             C::CP >= (a.out_type == MOE_DTYPE_F32 ? 8 : 16);
+        if (sectors) {
+          if (dst >= 0) {
+            if (a.out_type == MOE_DTYPE_F32) store_sectors<C::CP>(static_cast<float*>(a.out), a.N, n0, v, dst);
+            else if (a.out_type == MOE_DTYPE_BF16) store_sectors<C::CP>(static_cast<__nv_bfloat16*>(a.out), a.N, n0, v, dst);
+            else store_sectors<C::CP>(static_cast<__half*>(a.out), a.N, n0, v, dst);
+          }
+        } else {
+          const int word = a.N % 4 == 0 ? 4 : a.N % 2 == 0 ? 2 : 1;  // columns that stay aligned in every row
+          store_tile<C::CP>(a.out, a.out_type, word, a.N, n0, v, stg, dst);
+        }
       }
     }
     finish();
@@ -832,7 +868,7 @@ cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   const long long most = device_info().sm_count / C::S;
   cfg.gridDim = dim3(unsigned((max_tiles < most ? max_tiles : most) * C::S));
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
