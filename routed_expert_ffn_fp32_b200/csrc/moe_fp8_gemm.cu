@@ -63,9 +63,9 @@ struct Cfg {
   static constexpr int TMEM = BN * KU * BUFS;
   static constexpr int PROMOTERS = MR == 16 ? 2 : EW;
   static constexpr int XCH_BYTES = SWIGLU ? 2 * PARTS * S * MR * 4 : 0;  // [2][PARTS S][MR] maxima
-  // MR = 16: a tile's sums.  Otherwise per lane 8 values on their way out, the
-  // lane's output row and the tile's column block, and padding.
-  static constexpr int STG_PITCH = SWIGLU ? 2 : 11;
+  // MR = 16: a tile's sums.  Otherwise per lane 16 values on their way out, then
+  // the lane's output row and the tile's column block.
+  static constexpr int STG_PITCH = SWIGLU ? 2 : 20;
   static constexpr int STG_BYTES = MR == 16 ? 16 * (BN + 4) * 4 : EW * 32 * STG_PITCH * 4;
   static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
   static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 14 * 1024) / (A_BYTES + B_BYTES);
@@ -161,6 +161,7 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
 template <int CP, typename T>
 __device__ __forceinline__ void store_sectors(T* out, int N, int n0, const float2 (&v)[CP / 2], int dst) {
   constexpr int E = 32 / sizeof(T);
+  if constexpr (CP < E) return;  // never launched
   T* o = out + size_t(dst) * N + n0;
 #pragma unroll
   for (int c = 0; c < CP / E; ++c) {
@@ -175,43 +176,48 @@ __device__ __forceinline__ void store_sectors(T* out, int N, int n0, const float
   }
 }
 
+// W consecutive values of one row
+template <int W>
+__device__ __forceinline__ void store_word(void* out, int type, size_t o, const float* f) {
+  if constexpr (W == 1) {
+    store_one(out, type, o, f[0]);
+  } else if (type == MOE_DTYPE_F32) {
+    float* d = static_cast<float*>(out) + o;
+    if constexpr (W == 4) *reinterpret_cast<float4*>(d) = *reinterpret_cast<const float4*>(f);
+    else *reinterpret_cast<float2*>(d) = *reinterpret_cast<const float2*>(f);
+  } else {
+    uint16_t* d = static_cast<uint16_t*>(out) + o;
+    if constexpr (W == 4) *reinterpret_cast<uint2*>(d) = make_uint2(pack16(type, f[0], f[1]), pack16(type, f[2], f[3]));
+    else *reinterpret_cast<uint32_t*>(d) = pack16(type, f[0], f[1]);
+  }
+}
+
 // A warp's 32 rows x CP columns (lane l: row l in v, its output row dst or -1)
-// to rows of any width N.  They pass through shared memory 8 columns at a time,
-// so that a store covers runs of several rows' neighbours instead of one word
-// in each of 32; word: columns a lane stores at once (4, 2 or 1, N a multiple).
-template <int CP>
-__device__ __forceinline__ void store_tile(void* out, int type, int word, int N, int n0, const float2 (&v)[CP / 2],
-                                           float* stg, int dst) {
-  constexpr int PITCH = 11, PC = 8;
-  const int lane = threadIdx.x & 31;
-  const int lpr = PC / word, rpi = 32 / lpr;  // lanes per row, rows per store
-  const int j = word * (lane % lpr), r0 = lane / lpr;
+// to rows of any width N, a multiple of W.  They pass through shared memory 16
+// columns at a time, so that a store covers runs of a few rows instead of one
+// word in each of 32.
+template <int W, int CP>
+__device__ __forceinline__ void store_tile(void* out, int type, int N, int n0, const float2 (&v)[CP / 2], float* stg,
+                                           int dst) {
+  constexpr int PITCH = 20, PC = CP < 16 ? CP : 16, LPR = PC / W, RPI = 32 / LPR;  // lanes per row, rows per store
+  const int lane = threadIdx.x & 31, j = W * (lane % LPR), r0 = lane / LPR;
+  int drow[LPR];
+#pragma unroll
+  for (int i = 0; i < LPR; ++i) drow[i] = __shfl_sync(kFull, dst, i * RPI + r0);
 #pragma unroll
   for (int c = 0; c < CP / PC; ++c) {
     if (n0 + c * PC >= N) break;
 #pragma unroll
-    for (int k = 0; k < PC; ++k) stg[lane * PITCH + k] = k & 1 ? v[(c * PC + k) / 2].y : v[(c * PC + k) / 2].x;
+    for (int k = 0; k < PC / 4; ++k)
+      *reinterpret_cast<float4*>(stg + lane * PITCH + 4 * k) =
+          make_float4(v[c * PC / 2 + 2 * k].x, v[c * PC / 2 + 2 * k].y, v[c * PC / 2 + 2 * k + 1].x,
+                      v[c * PC / 2 + 2 * k + 1].y);
     __syncwarp();
     const int n = n0 + c * PC + j;
-#pragma unroll 1
-    for (int i = 0; i < lpr; ++i) {
-      const int r = i * rpi + r0;
-      const int drow = __shfl_sync(kFull, dst, r);
-      if (drow < 0 || n >= N) continue;
-      const float* f = stg + r * PITCH + j;
-      const size_t o = size_t(drow) * N + n;
-      if (word == 1) {
-        store_one(out, type, o, f[0]);
-      } else if (type == MOE_DTYPE_F32) {
-        float* d = static_cast<float*>(out) + o;
-        if (word == 4) *reinterpret_cast<float4*>(d) = make_float4(f[0], f[1], f[2], f[3]);
-        else *reinterpret_cast<float2*>(d) = make_float2(f[0], f[1]);
-      } else {
-        uint16_t* d = static_cast<uint16_t*>(out) + o;
-        if (word == 4) *reinterpret_cast<uint2*>(d) = make_uint2(pack16(type, f[0], f[1]), pack16(type, f[2], f[3]));
-        else *reinterpret_cast<uint32_t*>(d) = pack16(type, f[0], f[1]);
-      }
-    }
+#pragma unroll
+    for (int i = 0; i < LPR; ++i)
+      if (drow[i] >= 0 && n < N)
+        store_word<W>(out, type, size_t(drow[i]) * N + n, stg + (i * RPI + r0) * PITCH + j);
     __syncwarp();
   }
 }
@@ -229,7 +235,8 @@ struct Ring {
   }
 };
 
-template <bool SWIGLU, int BN, int MR>
+// SECTORS: the output's rows are whole 32-byte sectors (or swiglu, or MR = 16).
+template <bool SWIGLU, int BN, int MR, bool SECTORS>
 __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
     k_gemm_fp8(const __grid_constant__ Fp8GemmArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<SWIGLU, BN, MR>;
@@ -359,6 +366,27 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
     }
   };
 
+  // Gathered rows: four at a time, one copy per lane.  A warp's lanes issue
+  // their copies one after the other, about 40 clocks each, so a full tile's 32
+  // copies are shared by the two producers (even groups of four, odd groups).
+  constexpr int GW = MR == 128 ? 2 : 1;
+  auto group_of = [&](int g) { return GW * lane + g; };
+  auto gather_rows = [&](const Tile& t, int g, int (&r)[4]) {
+    // positions past the bucket repeat its last row, an index out of range
+    // reads row 0
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int src = a.entries[t.row0 + min(4 * group_of(g) + j, t.nvalid - 1)] / a.a_div;
+      r[j] = src >= 0 && src < a.a_rows ? src : 0;
+    }
+  };
+  // bytes a producer's groups bring per K block
+  auto gather_bytes = [&](const Tile& t, int g) { return uint32_t(((t.nvalid + 3) / 4 - g + GW - 1) / GW * 512); };
+  auto gather_block = [&](const Tile& t, int g, const int (&r)[4], uint32_t to, int x, uint32_t fb) {
+    const int i = group_of(g);
+    if (i < MR / 4 && 4 * i < t.nvalid) tma_gather4(to + i * 512, &maps.a, x, r[0], r[1], r[2], r[3], fb);
+  };
+
   if (warp >= kEpiWarps) {
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::KREG_LESS));
     if (warp == kEpiWarps) {
@@ -374,6 +402,10 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
         // weights that one row tile alone reads are not worth keeping in L2
         const uint64_t pol = t_beg[t.e + 1] - t_beg[t.e] <= MR ? once : keep;
         const int wrow = t.e * a.N + t.nt * C::COLS + rank * C::WBOX;
+        const bool rows = GW == 2 && gather;
+        int r[4] = {0, 0, 0, 0};
+        if (rows) gather_rows(t, 1, r);
+        const uint32_t bytes = C::B_BLK + (rows ? gather_bytes(t, 1) : 0);
         for (int kg = 0; kg < KG; ++kg, ring.next()) {
           ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 510);
           if (!ok) break;
@@ -384,7 +416,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
           if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kg == 0) continue;
           if (elect_one()) {
             const int kn = min(C::KU, KB - kg * C::KU);
-            bar_expect(fb, kn * C::B_BLK);
+            bar_expect(fb, kn * bytes);
 #pragma unroll
             for (int u = 0; u < C::KU; ++u) {
               if (u >= kn) break;
@@ -392,6 +424,14 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
               tma_2d(w + u * C::B_BLK, &maps.w[0], x, wrow, fb, pol);
               if (SWIGLU) tma_2d(w + u * C::B_BLK + C::WBOX * 128, &maps.w[1], x, wrow, fb, pol);
             }
+          }
+          __syncwarp();
+          if (rows) {
+            const uint32_t st = smem_addr(smem + ring.stage * C::A_BYTES);
+#pragma unroll
+            for (int u = 0; u < C::KU; ++u)
+              if (kg * C::KU + u < KB) gather_block(t, 1, r, st + u * C::A_BLK, (kg * C::KU + u) * 128, fb);
+            __syncwarp();
           }
           fills ^= 1u << ring.stage;
           used |= 1u << ring.stage;
@@ -414,20 +454,9 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
       bool ok = true;
       for (int it = first; it < n_tiles && ok; it += step) {
         const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
-        int r[4];
-        uint32_t bytes;
-        if (gather) {
-          // rows 4 lane .. 4 lane + 3 of the tile; positions past the bucket
-          // repeat its last row, an index out of range reads row 0
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int src = a.entries[t.row0 + min(4 * lane + j, t.nvalid - 1)] / a.a_div;
-            r[j] = src >= 0 && src < a.a_rows ? src : 0;
-          }
-          bytes = (t.nvalid + 3) / 4 * 512;
-        } else {
-          bytes = (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
-        }
+        int r[4] = {0, 0, 0, 0};
+        if (gather) gather_rows(t, 0, r);
+        const uint32_t bytes = gather ? gather_bytes(t, 0) : (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
         for (int kg = 0; kg < KG; ++kg, ring.next()) {
           ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 511);
           if (!ok) break;
@@ -441,7 +470,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
             const int x = (kg * C::KU + u) * 128;
             const uint32_t to = st + u * C::A_BLK;
             if (gather) {
-              if (4 * lane < t.nvalid) tma_gather4(to + lane * 512, &maps.a, x, r[0], r[1], r[2], r[3], fb);
+              gather_block(t, 0, r, to, x, fb);
             } else if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < MR / C::ABOX; ++j)
@@ -761,7 +790,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
     float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
     // what the tile's end needs waits in shared memory: the registers are the
     // accumulators'
-    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH) + (SWIGLU ? 0 : 8);
+    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH) + (SWIGLU ? 0 : 16);
     for (int it = first; it < n_tiles; it += step, ++local) {
       bool work;
       {
@@ -821,19 +850,19 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
         }
       } else if (work) {
         const int n0 = nt * BN + part * C::CP;
-        // rows of whole sectors: every lane stores its own row, 32 bytes a time
-        const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 &&
-                             a.N % (a.out_type == MOE_DTYPE_F32 ? 8 : 16) == 0 &&
-                             C::CP >= (a.out_type == MOE_DTYPE_F32 ? 8 : 16);
-        if (sectors) {
+        if constexpr (SECTORS) {
+          // every lane stores its own row, 32 bytes a time
           if (dst >= 0) {
             if (a.out_type == MOE_DTYPE_F32) store_sectors<C::CP>(static_cast<float*>(a.out), a.N, n0, v, dst);
             else if (a.out_type == MOE_DTYPE_BF16) store_sectors<C::CP>(static_cast<__nv_bfloat16*>(a.out), a.N, n0, v, dst);
             else store_sectors<C::CP>(static_cast<__half*>(a.out), a.N, n0, v, dst);
           }
         } else {
-          const int word = a.N % 4 == 0 ? 4 : a.N % 2 == 0 ? 2 : 1;  // columns that stay aligned in every row
-          store_tile<C::CP>(a.out, a.out_type, word, a.N, n0, v, stg, dst);
+          // words that stay aligned in every row.  (In a kernel of its own: its
+          // code costs the K loop registers, 142 -> 157 us on 4096 x 8192 x 4096.)
+          if (a.N % 4 == 0) store_tile<4, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
+          else if (a.N % 2 == 0) store_tile<2, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
+          else store_tile<1, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
         }
       }
     }
@@ -842,8 +871,8 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
 }
 
 // --------------------------------------------------------------- host side ---
-template <bool SWIGLU, int BN, int MR>
-cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
+template <bool SWIGLU, int BN, int MR, bool SECTORS>
+cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   using C = Cfg<SWIGLU, BN, MR>;
   Maps m;
   const uint64_t wrows = uint64_t(a.E) * a.N;
@@ -852,7 +881,7 @@ cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
     return cudaErrorInvalidValue;
   m.w[1] = m.w[0];
   if (SWIGLU && !make_tma_map_u8_box(&m.w[1], a.w_q[1], a.K, wrows, 128, C::WBOX)) return cudaErrorInvalidValue;
-  auto kern = k_gemm_fp8<SWIGLU, BN, MR>;
+  auto kern = k_gemm_fp8<SWIGLU, BN, MR, SECTORS>;
   const size_t smem = C::smem(a.E);
   // the kernel's shared-memory limit, set once per device
   static std::atomic<unsigned long long> set{0};
@@ -880,6 +909,16 @@ cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = C::S > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kern, a, m);
+}
+
+template <bool SWIGLU, int BN, int MR>
+cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
+  if constexpr (!SWIGLU && MR == 128) {
+    const int per = a.out_type == MOE_DTYPE_F32 ? 8 : 16;  // values in a sector
+    if ((reinterpret_cast<uintptr_t>(a.out) & 31u) != 0 || a.N % per != 0 || BN / 2 < per)
+      return launch_kernel<SWIGLU, BN, MR, false>(a, max_tiles, st);
+  }
+  return launch_kernel<SWIGLU, BN, MR, true>(a, max_tiles, st);
 }
 
 template <int MR>
