@@ -69,6 +69,10 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, bool swiglu, cudaStream_t st);
 bool make_tma_map_u8_box(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
                          uint32_t box_bytes, uint32_t box_rows);
 
+// The same matrix seen as [K / 128, rows, 128]: boxes of depth x box_rows x 128.
+bool make_tma_map_u8_deep(CUtensorMap* m, const void* base, uint64_t row_bytes, uint64_t rows,
+                          uint32_t box_rows, uint32_t depth);
+
 // --------------------------------------------------------------- primitives ---
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -156,6 +160,15 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+      : "memory");
+}
+// Blocks z.. of rows y.. (a map of make_tma_map_u8_deep).
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int z, int y, uint32_t bar,
+                                       uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4}], [%5], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "l"(policy)
       : "memory");
 }
 // Four rows of the matrix (a map with one-row boxes) into four consecutive

@@ -40,7 +40,9 @@ namespace {
 
 constexpr unsigned long long kLimitNs = 2000000000ull;  // default bound of a wait: 2 s
 
-template <bool SWIGLU, int BN, int MR>
+// SECTORS: the output's rows are whole 32-byte sectors (always with swiglu, or
+// MR = 16).
+template <bool SWIGLU, int BN, int MR, bool SECTORS>
 struct Cfg {
   static constexpr int S = SWIGLU ? 256 / BN : 1;    // CTAs that share a block of 128 columns
   static constexpr int COLS = SWIGLU ? 128 : BN;     // output columns per tile (of the cluster)
@@ -63,18 +65,19 @@ struct Cfg {
   static constexpr int TMEM = BN * KU * BUFS;
   static constexpr int PROMOTERS = MR == 16 ? 2 : EW;
   static constexpr int XCH_BYTES = SWIGLU ? 2 * PARTS * S * MR * 4 : 0;  // [2][PARTS S][MR] maxima
-  // MR = 16: a tile's sums.  Otherwise per lane 16 values on their way out, then
-  // the lane's output row and the tile's column block.
-  static constexpr int STG_PITCH = SWIGLU ? 2 : 20;
+  // MR = 16: a tile's sums.  Otherwise per lane the values of a store round
+  // (without SECTORS), then its output row and the tile's column block.
+  static constexpr int PC = CP < 16 || BN == 256 ? 8 : 16;
+  static constexpr int STG_PITCH = SECTORS ? 2 : PC + 4;
   static constexpr int STG_BYTES = MR == 16 ? 16 * (BN + 4) * 4 : EW * 32 * STG_PITCH * 4;
   static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
-  static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 14 * 1024) / (A_BYTES + B_BYTES);
+  static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 20 * 1024) / (A_BYTES + B_BYTES);
   static constexpr int NS = BN == 256 && MR == 128 ? 4 : FIT > 24 ? 24 : FIT;
-  // Scale slots: the rows' scales and the two weight scales of a K block.  The
-  // scale warp fills block g's slot once the MMAs of block g - NS are done, so
+  // Scale slots: sa * sw of every row of a K block, for the two column halves
+  // (or gate and up).  The scale warp fills block g's slot once the MMAs of block g - NS are done, so
   // the epilogue is past block g - NS - BUFS.
   static constexpr int SLOTS = NS + BUFS;
-  static constexpr int SLOT = MR + 4;                // floats, per K block
+  static constexpr int SLOT = 2 * MR;                // floats, per K block
   // the activation stages come first: an MR = 16 operand overruns into the
   // weight stages, never out of them
   static constexpr int W0 = NS * A_BYTES;
@@ -85,14 +88,18 @@ struct Cfg {
   static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + THREADS / 32) + 15) / 16 * 16;
   static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
   // registers of a promoting thread, and of the others (0: all the same)
-  static constexpr int KREG = BN == 256 ? 208 : 0, KREG_LESS = 88;
+  static constexpr int KREG = BN == 256 ? 216 : 0;
   static_assert(NS >= 3 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT && TMEM <= 512, "shared memory, TMEM");
   static size_t smem(int E) { return size_t(TAB) + 8 * size_t(E + 1) + 1024 /*alignment*/; }
 };
 
+// One box holds one K block of 128 bytes; with `deep` (K a multiple of 128) the
+// KU blocks of a stage, as a third dimension: one copy instead of KU, and a copy
+// costs its warp about 100 clocks.
 struct Maps {
   CUtensorMap a;     // A rows: 1-row boxes (gather) or ABOX-row boxes
   CUtensorMap w[2];  // weights, WBOX-row boxes (gate and up, or twice the same)
+  int deep;
 };
 
 struct Tile {
@@ -193,13 +200,13 @@ __device__ __forceinline__ void store_word(void* out, int type, size_t o, const 
 }
 
 // A warp's 32 rows x CP columns (lane l: row l in v, its output row dst or -1)
-// to rows of any width N, a multiple of W.  They pass through shared memory 16
+// to rows of any width N, a multiple of W.  They pass through shared memory PC
 // columns at a time, so that a store covers runs of a few rows instead of one
 // word in each of 32.
-template <int W, int CP>
+template <int W, int CP, int PC>
 __device__ __forceinline__ void store_tile(void* out, int type, int N, int n0, const float2 (&v)[CP / 2], float* stg,
                                            int dst) {
-  constexpr int PITCH = 20, PC = CP < 16 ? CP : 16, LPR = PC / W, RPI = 32 / LPR;  // lanes per row, rows per store
+  constexpr int PITCH = PC + 4, LPR = PC / W, RPI = 32 / LPR;  // lanes per row, rows per store
   const int lane = threadIdx.x & 31, j = W * (lane % LPR), r0 = lane / LPR;
   int drow[LPR];
 #pragma unroll
@@ -235,11 +242,10 @@ struct Ring {
   }
 };
 
-// SECTORS: the output's rows are whole 32-byte sectors (or swiglu, or MR = 16).
 template <bool SWIGLU, int BN, int MR, bool SECTORS>
-__global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
+__global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     k_gemm_fp8(const __grid_constant__ Fp8GemmArgs a, const __grid_constant__ Maps maps) {
-  using C = Cfg<SWIGLU, BN, MR>;
+  using C = Cfg<SWIGLU, BN, MR, SECTORS>;
   constexpr int S = C::S, kEpiWarps = C::EW, kThreads = C::THREADS;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(
@@ -388,9 +394,11 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
   };
 
   if (warp >= kEpiWarps) {
-    if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::KREG_LESS));
+    if constexpr (C::KREG != 0) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(504 - 2 * C::KREG));
     if (warp == kEpiWarps) {
       // ------------------------------------------------------ weight producer
+      // (a pair's gate and up rows alternate by K block, so it takes them singly)
+      constexpr bool DEEP_W = C::KU > 1 && !SWIGLU;
       Ring<C::NS> ring;
       uint32_t fills = 0, used = 0;
       uint64_t keep, once;
@@ -416,13 +424,18 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
           if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kg == 0) continue;
           if (elect_one()) {
             const int kn = min(C::KU, KB - kg * C::KU);
-            bar_expect(fb, kn * bytes);
+            if (DEEP_W && maps.deep) {  // blocks past K arrive as zeros
+              bar_expect(fb, C::B_BYTES + kn * (bytes - C::B_BLK));
+              tma_3d(w, &maps.w[0], kg * C::KU, wrow, fb, pol);
+            } else {
+              bar_expect(fb, kn * bytes);
 #pragma unroll
-            for (int u = 0; u < C::KU; ++u) {
-              if (u >= kn) break;
-              const int x = (kg * C::KU + u) * 128;
-              tma_2d(w + u * C::B_BLK, &maps.w[0], x, wrow, fb, pol);
-              if (SWIGLU) tma_2d(w + u * C::B_BLK + C::WBOX * 128, &maps.w[1], x, wrow, fb, pol);
+              for (int u = 0; u < C::KU; ++u) {
+                if (u >= kn) break;
+                const int x = (kg * C::KU + u) * 128;
+                tma_2d(w + u * C::B_BLK, &maps.w[0], x, wrow, fb, pol);
+                if (SWIGLU) tma_2d(w + u * C::B_BLK + C::WBOX * 128, &maps.w[1], x, wrow, fb, pol);
+              }
             }
           }
           __syncwarp();
@@ -448,6 +461,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
       }
     } else if (warp == kEpiWarps + 2) {
       // --------------------------------------------------------- row producer
+      constexpr bool DEEP_A = C::KU > 1 && MR == C::ABOX;  // a block's rows are one box
       Ring<C::NS> ring;
       uint64_t keep;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
@@ -462,8 +476,14 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
           if (!ok) break;
           const uint32_t st = smem_addr(smem + ring.stage * C::A_BYTES), fb = smem_addr(&full[ring.stage]);
           const int kn = min(C::KU, KB - kg * C::KU);
-          if (elect_one()) bar_expect(fb, kn * bytes);
+          const bool deep = DEEP_A && maps.deep && !gather;
+          if (elect_one()) bar_expect(fb, (deep ? C::KU : kn) * bytes);
           __syncwarp();
+          if (deep) {
+            if (elect_one()) tma_3d(st, &maps.a, kg * C::KU, t.row0, fb, keep);
+            __syncwarp();
+            continue;
+          }
 #pragma unroll
           for (int u = 0; u < C::KU; ++u) {
             if (u >= kn) break;
@@ -483,10 +503,10 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
       }
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
-      // lane l holds rows l, l + 32, ..; lanes 0 and 1 the two weight scales
-      // (the column halves' blocks, or gate and up).  UK K blocks a round, and
-      // the next round's loads in flight: their latency is several stages'.
-      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 8 : 4, UG = UK / C::KU;
+      // lane l holds rows l, l + 32, .. and both weight scales (the column
+      // halves' blocks, or gate and up).  UK K blocks a round, and the next
+      // round's loads in flight: their latency is several stages'.
+      constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 8 : 2, UG = UK / C::KU;
       Ring<C::NS> ring;
       Ring<C::SLOTS> slot;
       const int NB = fp8_blocks(a.N);
@@ -500,27 +520,32 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
           if (gather) src = a.entries[src] / a.a_div;
           sa[j] = a.a_s + size_t(src >= 0 && src < a.a_rows ? src : 0) * KB;
         }
-        const int h = lane & 1;
-        const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * (BN / 2)) / kFp8Block, NB - 1);
-        const float* sw = a.w_s[SWIGLU ? h : 0] + (size_t(t.e) * NB + nb) * KB;
-        float next_a[UK][RJ], next_w[UK];
+        const float* sw[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int nb = SWIGLU ? t.nt : min((t.nt * BN + h * (BN / 2)) / kFp8Block, NB - 1);
+          sw[h] = a.w_s[SWIGLU ? h : 0] + (size_t(t.e) * NB + nb) * KB;
+        }
+        float next_a[UK][RJ], next_w[UK][2];
         auto load = [&](int kg) {
 #pragma unroll
           for (int u = 0; u < UK; ++u) {
             const int k = min(kg * C::KU + u, KB - 1);
 #pragma unroll
             for (int j = 0; j < RJ; ++j) next_a[u][j] = sa[j][k];
-            next_w[u] = sw[k];
+            next_w[u][0] = sw[0][k];
+            next_w[u][1] = sw[1][k];
           }
         };
         load(0);
         for (int kg = 0; kg < KG && ok; kg += UG) {
-          float va[UK][RJ], vw[UK];
+          float va[UK][RJ], vw[UK][2];
 #pragma unroll
           for (int u = 0; u < UK; ++u) {
 #pragma unroll
             for (int j = 0; j < RJ; ++j) va[u][j] = next_a[u][j];
-            vw[u] = next_w[u];
+            vw[u][0] = next_w[u][0];
+            vw[u][1] = next_w[u][1];
           }
           if (kg + UG < KG) load(kg + UG);
 #pragma unroll
@@ -531,10 +556,13 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
 #pragma unroll
             for (int u = 0; u < C::KU; ++u) {
               float* to = scl + (slot.stage * C::KU + u) * C::SLOT;
+              const int i = g * C::KU + u;
 #pragma unroll
               for (int j = 0; j < RJ; ++j)
-                if (MR >= 32 || lane < MR) to[lane + 32 * j] = va[g * C::KU + u][j];
-              if (lane < 2) to[MR + lane] = vw[g * C::KU + u];
+                if (MR >= 32 || lane < MR) {
+                  to[lane + 32 * j] = va[i][j] * vw[i][0];
+                  to[MR + lane + 32 * j] = va[i][j] * vw[i][1];
+                }
             }
             __syncwarp();
             if (lane == 0) {
@@ -607,25 +635,20 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
 #pragma unroll
       for (int j = 0; j < C::CP / 2; ++j) v[j] = make_float2(0.f, 0.f);
       float s0[C::KU], s1[C::KU];
-      auto scales = [&] {  // of the next stage in turn
+      auto scales = [&] {
         if (!bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531)) return false;
-        const float* sc = scl + slot.stage * C::KU * C::SLOT;
+        const float* sc = scl + slot.stage * C::KU * C::SLOT + (MR >= 128 ? row : row & (MR - 1));
 #pragma unroll
         for (int u = 0; u < C::KU; ++u) {
-          const float s_row = sc[u * C::SLOT + (MR >= 128 ? row : row & (MR - 1))];
-          s0[u] = s_row * sc[u * C::SLOT + MR + (SWIGLU ? 0 : part / (C::PARTS / 2))];
-          s1[u] = SWIGLU ? s_row * sc[u * C::SLOT + MR + 1] : 0.f;
+          s0[u] = sc[u * C::SLOT + (SWIGLU ? 0 : part * MR)];
+          s1[u] = SWIGLU ? sc[u * C::SLOT + MR] : 0.f;
         }
         slot.next();
         return true;
       };
-      // (small buckets read the scales a stage ahead; the full tile has no
-      // registers left for that)
-      constexpr bool AHEAD = MR == 16;
-      if (AHEAD && !scales()) return false;
       for (int kg = 0; kg < KG; ++kg, acc.next()) {
         const int kn = min(C::KU, KB - kg * C::KU);
-        if (!AHEAD && !scales()) return false;
+        if (!scales()) return false;
         if (!bar_wait(smem_addr(&acc_full[acc.stage]), acc.phase, ctl, 530)) return false;
         auto release = [&] {  // the MMAs may have the buffer
           tcgen_fence_before();
@@ -644,6 +667,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
               uint32_t d[UB][CH];
 #pragma unroll
               for (int u = 0; u < UB; ++u) tmem_load<CH>(col + (u0 + u) * BN + at(c * CH), d[u]);
+              // the next stage's scales while the first sums arrive
 #pragma unroll
               for (int u = 0; u < UB; ++u) tmem_wait<CH>(d[u]);
               if (c + 1 == NCH && u0 + UB >= C::KU) release();
@@ -660,7 +684,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
         } else {
           release();
         }
-        if (AHEAD && kg + 1 < KG && !scales()) return false;
       }
       return true;
     };
@@ -790,7 +813,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
     float* stg = reinterpret_cast<float*>(smem + C::STG) + warp * 32 * C::STG_PITCH;
     // what the tile's end needs waits in shared memory: the registers are the
     // accumulators'
-    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH) + (SWIGLU ? 0 : 16);
+    volatile int* park = reinterpret_cast<volatile int*>(stg + lane * C::STG_PITCH) + (SECTORS ? 0 : C::PC);
     for (int it = first; it < n_tiles; it += step, ++local) {
       bool work;
       {
@@ -860,9 +883,9 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
         } else {
           // words that stay aligned in every row.  (In a kernel of its own: its
           // code costs the K loop registers, 142 -> 157 us on 4096 x 8192 x 4096.)
-          if (a.N % 4 == 0) store_tile<4, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
-          else if (a.N % 2 == 0) store_tile<2, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
-          else store_tile<1, C::CP>(a.out, a.out_type, a.N, n0, v, stg, dst);
+          if (a.N % 4 == 0) store_tile<4, C::CP, C::PC>(a.out, a.out_type, a.N, n0, v, stg, dst);
+          else if (a.N % 2 == 0) store_tile<2, C::CP, C::PC>(a.out, a.out_type, a.N, n0, v, stg, dst);
+          else store_tile<1, C::CP, C::PC>(a.out, a.out_type, a.N, n0, v, stg, dst);
         }
       }
     }
@@ -871,16 +894,26 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR>::THREADS, 1)
 }
 
 // --------------------------------------------------------------- host side ---
+// Map of a [rows, K] code matrix: boxes of box_rows x 128 bytes (128-byte
+// swizzle); depth > 0 (K a multiple of 128): boxes of `depth` neighbouring K
+// blocks, one block's rows after the other's.
+bool make_map(CUtensorMap* m, const uint8_t* base, uint64_t K, uint64_t rows, uint32_t box_rows, uint32_t depth) {
+  if (depth == 0) return make_tma_map_u8_box(m, base, K, rows, 128, box_rows);
+  return make_tma_map_u8_deep(m, base, K, rows, box_rows, depth);
+}
+
 template <bool SWIGLU, int BN, int MR, bool SECTORS>
 cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
-  using C = Cfg<SWIGLU, BN, MR>;
+  using C = Cfg<SWIGLU, BN, MR, SECTORS>;
   Maps m;
   const uint64_t wrows = uint64_t(a.E) * a.N;
-  if (!make_tma_map_u8_box(&m.a, a.a_q, a.K, a.a_rows, 128, a.a_div > 0 ? 1 : C::ABOX) ||
-      !make_tma_map_u8_box(&m.w[0], a.w_q[0], a.K, wrows, 128, C::WBOX))
+  m.deep = C::KU > 1 && a.K % 128 == 0;
+  const bool deep_a = m.deep && C::ABOX == MR && a.a_div == 0, deep_w = m.deep && !SWIGLU;
+  if (!make_map(&m.a, a.a_q, a.K, a.a_rows, a.a_div > 0 ? 1 : C::ABOX, deep_a ? C::KU : 0) ||
+      !make_map(&m.w[0], a.w_q[0], a.K, wrows, C::WBOX, deep_w ? C::KU : 0))
     return cudaErrorInvalidValue;
   m.w[1] = m.w[0];
-  if (SWIGLU && !make_tma_map_u8_box(&m.w[1], a.w_q[1], a.K, wrows, 128, C::WBOX)) return cudaErrorInvalidValue;
+  if (SWIGLU && !make_map(&m.w[1], a.w_q[1], a.K, wrows, C::WBOX, 0)) return cudaErrorInvalidValue;
   auto kern = k_gemm_fp8<SWIGLU, BN, MR, SECTORS>;
   const size_t smem = C::smem(a.E);
   // the kernel's shared-memory limit, set once per device
