@@ -25,11 +25,11 @@
 // keeps 2 KB of activations and the MMA's other 112 rows read whatever lies
 // behind (rows of a product do not mix, and nobody reads theirs).
 //
-// Few rows mean few tiles, so the tile gets narrower (down to 16 weight rows)
-// until every SM streams its own weights; K is never split, so nothing has to
-// be joined.  The fused pair needs the largest |h| of each 128 columns: its
-// narrow tiles form a cluster of 2, 4 or 8 CTAs that share such a block and
-// exchange each row's maximum through distributed shared memory.
+// Few rows mean few tiles, so the tile gets narrower (down to 64 weight rows)
+// to spread the weights over more SMs; K is never split, so nothing has to be
+// joined.  The fused pair needs the largest |h| of each 128 columns: its narrow
+// tiles form a cluster of 2 or 4 CTAs that share such a block and exchange each
+// row's maximum through distributed shared memory.
 #include <atomic>
 #include <type_traits>
 
@@ -58,7 +58,7 @@ struct Cfg {
   static constexpr int THREADS = (EW + 4) * 32;
   static constexpr int CP = BN / PARTS;              // accumulator columns per thread
   // columns per TMEM load: two loads' registers beside the accumulators
-  static constexpr int CH = CP == 128 ? 16 : CP == 64 ? 32 : SWIGLU ? CP / 2 : CP;
+  static constexpr int CH = CP == 128 || (SWIGLU && CP == 32) ? 16 : 32;
   static constexpr int UB = KU * CH > 64 ? 64 / CH : KU;  // K blocks per round of TMEM loads
   // TMEM accumulator sets, one accumulator per K block of a stage
   static constexpr int BUFS = BN * KU >= 256 ? 2 : 4;
@@ -67,7 +67,7 @@ struct Cfg {
   static constexpr int XCH_BYTES = SWIGLU ? 2 * PARTS * S * MR * 4 : 0;  // [2][PARTS S][MR] maxima
   // MR = 16: a tile's sums.  Otherwise per lane the values of a store round
   // (without SECTORS), then its output row and the tile's column block.
-  static constexpr int PC = CP < 16 || BN == 256 ? 8 : 16;
+  static constexpr int PC = BN == 256 ? 8 : 16;
   static constexpr int STG_PITCH = SECTORS ? 2 : PC + 4;
   static constexpr int STG_BYTES = MR == 16 ? 16 * (BN + 4) * 4 : EW * 32 * STG_PITCH * 4;
   static constexpr int LIMIT = 227 * 1024 - 8 * (kMaxExperts + 1) - 1024;  // less tables, alignment
@@ -101,6 +101,11 @@ struct Maps {
   CUtensorMap w[2];  // weights, WBOX-row boxes (gate and up, or twice the same)
   int deep;
 };
+
+// Rows fetched four at a time: picked by the entries, or too few to fill a box
+// (a box that runs past the matrix is slow: T = 1, N = 2048, K = 4096 took
+// 12.5 us with 16-row boxes, 8.7 us so).
+__host__ __device__ inline bool rows_by_four(const Fp8GemmArgs& a) { return a.a_div > 0 || a.P < 16; }
 
 struct Tile {
   int e, nt;
@@ -168,7 +173,6 @@ __device__ __forceinline__ void st_sector(void* p, const uint32_t (&w)[8]) {
 template <int CP, typename T>
 __device__ __forceinline__ void store_sectors(T* out, int N, int n0, const float2 (&v)[CP / 2], int dst) {
   constexpr int E = 32 / sizeof(T);
-  if constexpr (CP < E) return;  // never launched
   T* o = out + size_t(dst) * N + n0;
 #pragma unroll
   for (int c = 0; c < CP / E; ++c) {
@@ -354,7 +358,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
   const int n_tiles = t_off[a.E];
   const int KB = fp8_blocks(a.K), KG = (KB + C::KU - 1) / C::KU;  // K blocks, stages of them
   const int first = blockIdx.x / S, step = gridDim.x / S;
-  const bool gather = a.a_div > 0;
+  const bool gather = a.a_div > 0, by_row = rows_by_four(a);
   const WaitCtl ctl{abort_flag, a.err, wait_us ? wait_us * 1000ull : kLimitNs};
 
   // the end of every role.  (Each side of the register split calls it by itself
@@ -382,7 +386,8 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     // reads row 0
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int src = a.entries[t.row0 + min(4 * group_of(g) + j, t.nvalid - 1)] / a.a_div;
+      int src = t.row0 + min(4 * group_of(g) + j, t.nvalid - 1);
+      if (gather) src = a.entries[src] / a.a_div;
       r[j] = src >= 0 && src < a.a_rows ? src : 0;
     }
   };
@@ -410,7 +415,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
         // weights that one row tile alone reads are not worth keeping in L2
         const uint64_t pol = t_beg[t.e + 1] - t_beg[t.e] <= MR ? once : keep;
         const int wrow = t.e * a.N + t.nt * C::COLS + rank * C::WBOX;
-        const bool rows = GW == 2 && gather;
+        const bool rows = GW == 2 && by_row;
         int r[4] = {0, 0, 0, 0};
         if (rows) gather_rows(t, 1, r);
         const uint32_t bytes = C::B_BLK + (rows ? gather_bytes(t, 1) : 0);
@@ -469,14 +474,14 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       for (int it = first; it < n_tiles && ok; it += step) {
         const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
         int r[4] = {0, 0, 0, 0};
-        if (gather) gather_rows(t, 0, r);
-        const uint32_t bytes = gather ? gather_bytes(t, 0) : (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
+        if (by_row) gather_rows(t, 0, r);
+        const uint32_t bytes = by_row ? gather_bytes(t, 0) : (t.nvalid + C::ABOX - 1) / C::ABOX * C::ABOX * 128;
         for (int kg = 0; kg < KG; ++kg, ring.next()) {
           ok = bar_wait(smem_addr(&empty[ring.stage]), ring.phase ^ 1u, ctl, 511);
           if (!ok) break;
           const uint32_t st = smem_addr(smem + ring.stage * C::A_BYTES), fb = smem_addr(&full[ring.stage]);
           const int kn = min(C::KU, KB - kg * C::KU);
-          const bool deep = DEEP_A && maps.deep && !gather;
+          const bool deep = DEEP_A && maps.deep && !by_row;
           if (elect_one()) bar_expect(fb, (deep ? C::KU : kn) * bytes);
           __syncwarp();
           if (deep) {
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
             if (u >= kn) break;
             const int x = (kg * C::KU + u) * 128;
             const uint32_t to = st + u * C::A_BLK;
-            if (gather) {
+            if (by_row) {
               gather_block(t, 0, r, to, x, fb);
             } else if (elect_one()) {
 #pragma unroll
@@ -724,7 +729,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           if (!bar_wait(smem_addr(stg_full), local & 1u, ctl, 542)) break;
           if constexpr (SWIGLU) {
             // a warp per row, up to three of them; CPL columns per lane
-            constexpr int HC = BN / 2, CPL = HC < 32 ? 1 : HC / 32, HR = 3;
+            constexpr int HC = BN / 2, CPL = HC / 32, HR = 3;
             const int c = lane * CPL, n = t.nt * 128 + rank * HC + c;
             float h[HR][CPL], amax[HR];
 #pragma unroll
@@ -734,7 +739,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
 #pragma unroll
               for (int j = 0; j < CPL; ++j) {
                 h[i][j] = 0.f;
-                if (r < t.nvalid && c < HC && n + j < a.N)
+                if (r < t.nvalid && n + j < a.N)
                   h[i][j] = silu_mul(buf[r * PITCH + c + j], buf[r * PITCH + HC + c + j]);
                 amax[i] = fmaxf(amax[i], fabsf(h[i][j]));
               }
@@ -769,7 +774,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
               if (drow < 0) continue;
               const float s = fp8_scale(amax[i]), inv = 1.f / s;
               if (lane == 0 && rank == 0) a.s_out[size_t(drow) * NB + t.nt] = s;
-              if (c < HC && n < a.N) {  // N is a multiple of 16
+              if (n < a.N) {  // N is a multiple of 16
                 uint8_t* o = a.q_out + size_t(drow) * a.N + n;
                 if constexpr (CPL == 4)
                   *reinterpret_cast<uint32_t*>(o) =
@@ -861,15 +866,11 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           auto code4 = [&](int j) {
             return f32x4_to_e4m3x4(v[2 * j].x * inv, v[2 * j].y * inv, v[2 * j + 1].x * inv, v[2 * j + 1].y * inv);
           };
-          if constexpr (HP == 8) {
-            *reinterpret_cast<uint2*>(o) = make_uint2(code4(0), code4(1));
-          } else {
 #pragma unroll
-            for (int j = 0; j < HP / 16; ++j)
-              if (n0 + 16 * j < a.N)  // N is a multiple of 16
-                *reinterpret_cast<uint4*>(o + 16 * j) =
-                    make_uint4(code4(4 * j), code4(4 * j + 1), code4(4 * j + 2), code4(4 * j + 3));
-          }
+          for (int j = 0; j < HP / 16; ++j)
+            if (n0 + 16 * j < a.N)  // N is a multiple of 16
+              *reinterpret_cast<uint4*>(o + 16 * j) =
+                  make_uint4(code4(4 * j), code4(4 * j + 1), code4(4 * j + 2), code4(4 * j + 3));
         }
       } else if (work) {
         const int n0 = nt * BN + part * C::CP;
@@ -908,8 +909,8 @@ cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_
   Maps m;
   const uint64_t wrows = uint64_t(a.E) * a.N;
   m.deep = C::KU > 1 && a.K % 128 == 0;
-  const bool deep_a = m.deep && C::ABOX == MR && a.a_div == 0, deep_w = m.deep && !SWIGLU;
-  if (!make_map(&m.a, a.a_q, a.K, a.a_rows, a.a_div > 0 ? 1 : C::ABOX, deep_a ? C::KU : 0) ||
+  const bool four = rows_by_four(a), deep_a = m.deep && C::ABOX == MR && !four, deep_w = m.deep && !SWIGLU;
+  if (!make_map(&m.a, a.a_q, a.K, a.a_rows, four ? 1 : C::ABOX, deep_a ? C::KU : 0) ||
       !make_map(&m.w[0], a.w_q[0], a.K, wrows, C::WBOX, deep_w ? C::KU : 0))
     return cudaErrorInvalidValue;
   m.w[1] = m.w[0];
@@ -948,7 +949,7 @@ template <bool SWIGLU, int BN, int MR>
 cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   if constexpr (!SWIGLU && MR == 128) {
     const int per = a.out_type == MOE_DTYPE_F32 ? 8 : 16;  // values in a sector
-    if ((reinterpret_cast<uintptr_t>(a.out) & 31u) != 0 || a.N % per != 0 || BN / 2 < per)
+    if ((reinterpret_cast<uintptr_t>(a.out) & 31u) != 0 || a.N % per != 0)
       return launch_kernel<SWIGLU, BN, MR, false>(a, max_tiles, st);
   }
   return launch_kernel<SWIGLU, BN, MR, true>(a, max_tiles, st);
@@ -962,20 +963,30 @@ cudaError_t pick(const Fp8GemmArgs& a, bool swiglu, cudaStream_t st) {
   const long long rt = a.offsets ? groups + a.P / MR : (a.P + MR - 1) / MR;
   if (swiglu) {
     const long long t = rt * ((a.N + 127) / 128);
-    if (t * 8 <= sms) return launch<true, 32, MR>(a, t, st);
+    // a cluster shares a block of 128 columns while all clusters fit at once (T =
+    // 1, one expert of I = 2048, H = 4096: 10.0 us with 4 CTAs, 12.3 with 2, 17.0
+    // with 1, 18.6 with 8; T = 1, k = 4: 17.6 with 2, 18.8 with 1)
     if (t * 4 <= sms) return launch<true, 64, MR>(a, t, st);
     if (t * 2 <= sms) return launch<true, 128, MR>(a, t, st);
     return launch<true, 256, MR>(a, t, st);
   }
-  // One MMA takes as long for 16 weight rows as for 128, so the tile is the
-  // narrowest one whose tiles still fit the SMs at once; more work than that
-  // takes the widest (full tensor rate, fewest reads of the rows).
+  // An MMA costs about the same for 16 to 128 weight rows, and every column
+  // tile reads the rows again, so tiles below 64 columns lose what their number
+  // gains (T = 1, N = 4096, K = 2048: 9.2 us at 16 columns, 7.3 at 32, 6.6 at
+  // 64, 7.3 at 128).  Small buckets stream weights: 128 columns once the tiles
+  // outnumber the SMs (T = 5, k = 8, 256 experts of N = 4096, K = 2048: 55.2 us
+  // at 64, 51.6 at 128, 54.7 at 256).  Full tiles take the widest that still
+  // fills the SMs, or the narrowest that fits them at once (T = 300, N = 2048,
+  // K = 4096: 12.8 us at 64, 15.2 at 128; T = 512, N = 4096: 21.7 at 64, 17.0 at
+  // 128, 20.1 at 256).
   auto tiles = [&](int bn) { return rt * ((a.N + bn - 1) / bn); };
-  if (tiles(16) <= sms) return launch<false, 16, MR>(a, tiles(16), st);
-  if (tiles(32) <= sms) return launch<false, 32, MR>(a, tiles(32), st);
-  if (tiles(64) <= sms) return launch<false, 64, MR>(a, tiles(64), st);
-  if (tiles(128) <= sms) return launch<false, 128, MR>(a, tiles(128), st);
-  return launch<false, 256, MR>(a, tiles(256), st);
+  if constexpr (MR == 16) {
+    return tiles(128) > sms ? launch<false, 128, MR>(a, tiles(128), st) : launch<false, 64, MR>(a, tiles(64), st);
+  } else {
+    if (tiles(64) <= sms) return launch<false, 64, MR>(a, tiles(64), st);
+    if (tiles(128) <= sms) return launch<false, 128, MR>(a, tiles(128), st);
+    return launch<false, 256, MR>(a, tiles(256), st);
+  }
 }
 
 }  // namespace
