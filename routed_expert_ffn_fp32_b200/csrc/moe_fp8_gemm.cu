@@ -113,6 +113,19 @@ struct Tile {
   int nvalid;  // rows
 };
 
+// An MMA of M = 64 keeps row r in lane r % 16 of TMEM quarter r / 16 (M = 128:
+// lane r % 32 of quarter r / 32).
+// The tensor cores then leave the rows alone that do not exist: at T = 2048 on
+// 256 experts, where the card runs at its power limit, 4 % less time.
+template <bool HALF>
+__device__ __forceinline__ bool half_tile(const Tile& t) { return HALF && t.nvalid <= 64; }
+// Row of a TMEM lane; past every tile for the lanes that hold none.
+template <bool HALF>
+__device__ __forceinline__ int row_at(const Tile& t, int place) {
+  if (!half_tile<HALF>(t)) return place;
+  return (place & 16) ? 1 << 20 : place / 32 * 16 + (place & 15);
+}
+
 template <int MR>
 __device__ __forceinline__ Tile tile_of(const int* t_off, const int* t_beg, int E,
                                         int it) {
@@ -246,7 +259,9 @@ struct Ring {
   }
 };
 
-template <bool SWIGLU, int BN, int MR, bool SECTORS>
+// HALF: tiles of at most 64 rows run as MMAs of M = 64 (buckets; a dense product
+// has no use for it, and the code costs it 137 -> 148 us on 4096 x 8192 x 4096).
+template <bool SWIGLU, int BN, int MR, bool SECTORS, bool HALF>
 __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     k_gemm_fp8(const __grid_constant__ Fp8GemmArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<SWIGLU, BN, MR, SECTORS>;
@@ -358,7 +373,8 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
   const int n_tiles = t_off[a.E];
   const int KB = fp8_blocks(a.K), KG = (KB + C::KU - 1) / C::KU;  // K blocks, stages of them
   const int first = blockIdx.x / S, step = gridDim.x / S;
-  const bool gather = a.a_div > 0, by_row = rows_by_four(a);
+  const bool gather = a.a_div > 0, scatter = a.scatter;
+  const bool by_row = MR == 16 ? rows_by_four(a) : gather;
   const WaitCtl ctl{abort_flag, a.err, wait_us ? wait_us * 1000ull : kLimitNs};
 
   // the end of every role.  (Each side of the register split calls it by itself
@@ -508,7 +524,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       }
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
-      // lane l holds rows l, l + 32, .. and both weight scales (the column
+      // lane l holds the rows of TMEM lanes l, l + 32, .. and both weight scales (the column
       // halves' blocks, or gate and up).  UK K blocks a round, and the next
       // round's loads in flight: their latency is several stages'.
       constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 8 : 2, UG = UK / C::KU;
@@ -521,7 +537,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
         const float* sa[RJ];
 #pragma unroll
         for (int j = 0; j < RJ; ++j) {
-          int src = t.row0 + min(lane + 32 * j, t.nvalid - 1);
+          int src = t.row0 + min(row_at<HALF>(t, lane + 32 * j), t.nvalid - 1);
           if (gather) src = a.entries[src] / a.a_div;
           sa[j] = a.a_s + size_t(src >= 0 && src < a.a_rows ? src : 0) * KB;
         }
@@ -586,13 +602,15 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       Ring<C::NS> ring;
       Ring<C::BUFS> acc;
       bool ok = true;
-      constexpr uint32_t idesc = idesc_e4m3(MR == 16 ? 64 : 128, BN);
       const uint64_t da0 = desc_k_sw128(smem_addr(smem)), dw0 = desc_k_sw128(smem_addr(smem + C::W0));
-      for (int it = first; it < n_tiles && ok; it += step) {
+      // one tile's MMAs, with a constant descriptor: a variable one cost 7 % of
+      // the whole product
+      auto issue = [&](auto m) {
+        constexpr uint32_t idesc = idesc_e4m3(decltype(m)::value, BN);
         for (int kg = 0; kg < KG; ++kg, ring.next(), acc.next()) {
           ok = bar_wait(smem_addr(&acc_empty[acc.stage]), acc.phase ^ 1u, ctl, 520) &&
                bar_wait(smem_addr(&full[ring.stage]), ring.phase, ctl, 521);
-          if (!ok) break;
+          if (!ok) return;
           tcgen_fence_after();
           const int left = a.K - kg * C::KU * 128;  // a tail of K reads zero fill to its next 32
           if (elect_one()) {
@@ -612,6 +630,10 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           }
           __syncwarp();
         }
+      };
+      for (int it = first; it < n_tiles && ok; it += step) {
+        if (MR == 16 || half_tile<HALF>(tile_of<MR>(t_off, t_beg, a.E, it))) issue(std::integral_constant<int, 64>{});
+        else issue(std::integral_constant<int, 128>{});
       }
       if (!ok || *abort_flag) {
         // let issued MMAs finish before TMEM is released (bounded)
@@ -626,7 +648,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     // --------------------------------------------------- promotion, epilogue
     if constexpr (C::KREG != 0) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::KREG));
     const int q = warp & 3, part = warp >> 2;
-    const int row = 32 * q + lane;
+    const int place = 32 * q + lane;  // TMEM lane: scale slots and maxima go by it
     const int NB = fp8_blocks(a.N);
     Ring<C::BUFS> acc;
     Ring<C::SLOTS> slot;
@@ -642,7 +664,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       float s0[C::KU], s1[C::KU];
       auto scales = [&] {
         if (!bar_wait(smem_addr(&scl_full[slot.stage]), slot.phase, ctl, 531)) return false;
-        const float* sc = scl + slot.stage * C::KU * C::SLOT + (MR >= 128 ? row : row & (MR - 1));
+        const float* sc = scl + slot.stage * C::KU * C::SLOT + (MR >= 128 ? place : place & (MR - 1));
 #pragma unroll
         for (int u = 0; u < C::KU; ++u) {
           s0[u] = sc[u * C::SLOT + (SWIGLU ? 0 : part * MR)];
@@ -695,13 +717,13 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     // output row of bucket position p, or -1 (latched) for an entry that names
     // no row
     auto out_row = [&](int p) {
-      if (!gather && !a.scatter) return p;
+      if (!gather && !scatter) return p;
       const int ent = a.entries[p];
-      if (ent < 0 || (gather && ent / a.a_div >= a.a_rows) || (a.scatter && ent >= a.P)) {
+      if (ent < 0 || (gather && ent / a.a_div >= a.a_rows) || (scatter && ent >= a.P)) {
         latch_error(a.err, MOE_ERR_DEVICE_DATA, 501);
         return -1;
       }
-      return a.scatter ? ent : p;
+      return scatter ? ent : p;
     };
     if constexpr (MR == 16) {
       // Only TMEM quarter 0 holds rows: its two warps promote, leave the tile in
@@ -823,8 +845,9 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       bool work;
       {
         const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
-        work = 32 * q < t.nvalid;
-        park[0] = row < t.nvalid ? out_row(t.row0 + row) : -1;
+        const int r = row_at<HALF>(t, place);
+        work = row_at<HALF>(t, 32 * q) < t.nvalid;
+        park[0] = r < t.nvalid ? out_row(t.row0 + r) : -1;
         park[1] = t.nt;
       }
       float2 v[C::CP / 2];
@@ -844,7 +867,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           if (n0 + 2 * j < a.N) amax = fmaxf(amax, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
         }
         float* x = xch + (local & 1u) * (C::PARTS * S * MR);
-        float* mine = x + (C::PARTS * rank + part) * MR + row;
+        float* mine = x + (C::PARTS * rank + part) * MR + place;
         if constexpr (S > 1) {
 #pragma unroll
           for (int k = 0; k < S; ++k) cluster_st(cluster_map(smem_addr(mine), k), amax);
@@ -858,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
         }
         if (!bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540)) break;
 #pragma unroll
-        for (int k = 0; k < C::PARTS * S; ++k) amax = fmaxf(amax, x[k * MR + row]);
+        for (int k = 0; k < C::PARTS * S; ++k) amax = fmaxf(amax, x[k * MR + place]);
         if (dst >= 0 && n0 < a.N) {
           const float s = fp8_scale(amax), inv = 1.f / s;
           if (part == 0 && rank == 0) a.s_out[size_t(dst) * NB + nt] = s;
@@ -903,7 +926,7 @@ bool make_map(CUtensorMap* m, const uint8_t* base, uint64_t K, uint64_t rows, ui
   return make_tma_map_u8_deep(m, base, K, rows, box_rows, depth);
 }
 
-template <bool SWIGLU, int BN, int MR, bool SECTORS>
+template <bool SWIGLU, int BN, int MR, bool SECTORS, bool HALF>
 cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   using C = Cfg<SWIGLU, BN, MR, SECTORS>;
   Maps m;
@@ -915,7 +938,7 @@ cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_
     return cudaErrorInvalidValue;
   m.w[1] = m.w[0];
   if (SWIGLU && !make_map(&m.w[1], a.w_q[1], a.K, wrows, C::WBOX, 0)) return cudaErrorInvalidValue;
-  auto kern = k_gemm_fp8<SWIGLU, BN, MR, SECTORS>;
+  auto kern = k_gemm_fp8<SWIGLU, BN, MR, SECTORS, HALF>;
   const size_t smem = C::smem(a.E);
   // the kernel's shared-memory limit, set once per device
   static std::atomic<unsigned long long> set{0};
@@ -949,10 +972,13 @@ template <bool SWIGLU, int BN, int MR>
 cudaError_t launch(const Fp8GemmArgs& a, long long max_tiles, cudaStream_t st) {
   if constexpr (!SWIGLU && MR == 128) {
     const int per = a.out_type == MOE_DTYPE_F32 ? 8 : 16;  // values in a sector
-    if ((reinterpret_cast<uintptr_t>(a.out) & 31u) != 0 || a.N % per != 0)
-      return launch_kernel<SWIGLU, BN, MR, false>(a, max_tiles, st);
+    const bool sectors = (reinterpret_cast<uintptr_t>(a.out) & 31u) == 0 && a.N % per == 0;
+    if (a.offsets == nullptr)
+      return sectors ? launch_kernel<false, BN, MR, true, false>(a, max_tiles, st)
+                     : launch_kernel<false, BN, MR, false, false>(a, max_tiles, st);
+    if (!sectors) return launch_kernel<false, BN, MR, false, true>(a, max_tiles, st);
   }
-  return launch_kernel<SWIGLU, BN, MR, true>(a, max_tiles, st);
+  return launch_kernel<SWIGLU, BN, MR, true, true>(a, max_tiles, st);
 }
 
 template <int MR>
