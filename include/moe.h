@@ -351,8 +351,7 @@ MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_
  *
  * The last block of a dimension may be short.  A value is code times scale; a
  * product sums each block of 128 in the tensor core's float32 accumulator and
- * the blocks, times both scales, in float32, in ascending order (in up to 8
- * ranges of K, added in order, when there are few rows).  Quantised outputs
+ * the blocks, times both scales, in float32, in ascending order.  Quantised outputs
  * take s = max(max|v| / 448, 2^-126) over a block's values that are not NaN,
  * and code = E4M3(v / s), rounded to nearest even; a NaN stays NaN.
  *

@@ -22,8 +22,21 @@
 //              bucket's entries, or boxes of consecutive rows
 //   warp 11    the scales of each K block, through shared memory
 // Only rows that exist are fetched.  Small buckets take MR = 16: the stage
-// keeps 2 KB of activations and the MMA's other 112 rows read whatever lies
-// behind (rows of a product do not mix, and nobody reads theirs).
+// keeps 2 KB of activations and the other 48 rows of an M = 64 MMA read whatever
+// lies behind (rows of a product do not mix, and nobody reads theirs); two warps
+// promote and the other six store the tile before.
+//
+// What bounds it (B200, K loop of the full tile, per K block of 128): the MMAs
+// and the copies of a 128 x 256 tile move 48 KB into and 48 KB out of shared
+// memory, about 750 clocks without any promotion (106 us for 4096 x 8192 x
+// 4096); with it 137 us, 2.0 PFLOP/s, as the promoting warps' chain of wait,
+// TMEM load and FMA is the longer one (TMEM loads alone cost nothing, half the
+// FMAs saves 10 us, the scales 10 us).  Grouped products of many experts are
+// bound by HBM: down, T = 5, k = 8, 256 experts, H = 4096, I = 2048: 53 us for
+// 316 MB (6.0 TB/s); T = 2048: 385 us (6.0 TB/s); gate / up T = 1: 26.3 us for
+// 134 MB (5.1 TB/s), T = 2048: 890 us (4.9 TB/s, TMA row gather and the tile's
+// end beside the weights).  Under a sustained load the card's power limit lowers
+// the clock, and the full tiles follow it (163, 455 and 935 us).
 //
 // Few rows mean few tiles, so the tile gets narrower (down to 64 weight rows)
 // to spread the weights over more SMs; K is never split, so nothing has to be
@@ -57,7 +70,7 @@ struct Cfg {
   static constexpr int PARTS = EW / 4;
   static constexpr int THREADS = (EW + 4) * 32;
   static constexpr int CP = BN / PARTS;              // accumulator columns per thread
-  // columns per TMEM load: two loads' registers beside the accumulators
+  // columns per TMEM load: what fits in registers beside the accumulators
   static constexpr int CH = CP == 128 || (SWIGLU && CP == 32) ? 16 : 32;
   static constexpr int UB = KU * CH > 64 ? 64 / CH : KU;  // K blocks per round of TMEM loads
   // TMEM accumulator sets, one accumulator per K block of a stage
@@ -74,8 +87,8 @@ struct Cfg {
   static constexpr int FIT = (LIMIT - STG_BYTES - XCH_BYTES - 20 * 1024) / (A_BYTES + B_BYTES);
   static constexpr int NS = BN == 256 && MR == 128 ? 4 : FIT > 24 ? 24 : FIT;
   // Scale slots: sa * sw of every row of a K block, for the two column halves
-  // (or gate and up).  The scale warp fills block g's slot once the MMAs of block g - NS are done, so
-  // the epilogue is past block g - NS - BUFS.
+  // (or gate and up).  The scale warp fills block g's slot once the MMAs of
+  // block g - NS are done, so the epilogue is past block g - NS - BUFS.
   static constexpr int SLOTS = NS + BUFS;
   static constexpr int SLOT = 2 * MR;                // floats, per K block
   // the activation stages come first: an MR = 16 operand overruns into the
@@ -87,7 +100,8 @@ struct Cfg {
   static constexpr int CTL = SCL + SLOTS * KU * SLOT * 4; // barriers and flags
   static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + THREADS / 32) + 15) / 16 * 16;
   static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
-  // registers of a promoting thread, and of the others (0: all the same)
+  // registers of a promoting thread (0: no split; the others get what is left of
+  // 3 x 168)
   static constexpr int KREG = BN == 256 ? 216 : 0;
   static_assert(NS >= 3 && NS * B_BYTES >= 128 * 128 && TAB <= LIMIT && TMEM <= 512, "shared memory, TMEM");
   static size_t smem(int E) { return size_t(TAB) + 8 * size_t(E + 1) + 1024 /*alignment*/; }
@@ -522,11 +536,18 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           __syncwarp();
         }
       }
+      // after a give-up: a stage's barrier may lack another producer, so these
+      // copies are given a millisecond to land
+      if (!ok || *abort_flag) {
+        const unsigned long long t0 = global_ns();
+        while (global_ns() - t0 < 1000000ull) {
+        }
+      }
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
-      // lane l holds the rows of TMEM lanes l, l + 32, .. and both weight scales (the column
-      // halves' blocks, or gate and up).  UK K blocks a round, and the next
-      // round's loads in flight: their latency is several stages'.
+      // lane l holds the rows of TMEM lanes l, l + 32, .. and both weight scales
+      // (the column halves' blocks, or gate and up).  UK K blocks a round, and
+      // the next round's loads in flight: their latency is several stages'.
       constexpr int RJ = (MR + 31) / 32, UK = MR == 16 ? 8 : 2, UG = UK / C::KU;
       Ring<C::NS> ring;
       Ring<C::SLOTS> slot;
@@ -603,8 +624,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       Ring<C::BUFS> acc;
       bool ok = true;
       const uint64_t da0 = desc_k_sw128(smem_addr(smem)), dw0 = desc_k_sw128(smem_addr(smem + C::W0));
-      // one tile's MMAs, with a constant descriptor: a variable one cost 7 % of
-      // the whole product
+      // one tile's MMAs
       auto issue = [&](auto m) {
         constexpr uint32_t idesc = idesc_e4m3(decltype(m)::value, BN);
         for (int kg = 0; kg < KG; ++kg, ring.next(), acc.next()) {
@@ -694,7 +714,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
               uint32_t d[UB][CH];
 #pragma unroll
               for (int u = 0; u < UB; ++u) tmem_load<CH>(col + (u0 + u) * BN + at(c * CH), d[u]);
-              // the next stage's scales while the first sums arrive
 #pragma unroll
               for (int u = 0; u < UB; ++u) tmem_wait<CH>(d[u]);
               if (c + 1 == NCH && u0 + UB >= C::KU) release();

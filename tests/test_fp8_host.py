@@ -156,3 +156,31 @@ def test_binding_refuses_shapes_and_types():
     if torch.cuda.is_available():
         with pytest.raises(ValueError, match="one device"):
             moe.moe_rmsnorm_quant_fp8(x.cuda(), _t(256, dtype=f32), 1e-6, _t(4, 256), _t(4, 2, dtype=f32))
+
+
+def test_binding_calls_on_the_tensors_device(monkeypatch):
+    """A call for tensors of another device than the current one runs with that
+    device current and on its stream."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 100 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+
+    def fn(*args):
+        seen.append((current[0], args))
+        return moe.MOE_OK
+
+    moe._call(fn, "x", 1, None, (7,))
+    moe._call(fn, "x", 0, None, (8,))
+    assert seen == [(1, (7, 101)), (0, (8, 100))] and current == [0]

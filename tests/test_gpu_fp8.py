@@ -6,9 +6,9 @@ products  The tensor core adds the 128 products of a block in four steps of 32
           to its float32 accumulator; a step loses at most one unit (2 u) of
           the largest partial sum for each of its 32 products and the
           accumulator, so a block at most 4 * 33 * 2 u of its terms' magnitude
-          sum.  Both scales multiply with one rounding each and every block,
-          and each of up to 8 ranges of K, is added with one more:
-          |err| <= (264 + blocks + 8 + 2) u M, M = sum |a w| scaled.
+          sum.  The two scales' product rounds once, and every block is scaled
+          and added with one more: |err| <= (264 + blocks + 2) u M, M = sum
+          |a w| scaled.
 norm      The sum of squares has only positive terms and meets at most 16 fmas
           per thread and chunk pair, 5 shuffle and 16 warp additions (< 64
           roundings); its root halves that; the reciprocal root is within 2
@@ -77,13 +77,15 @@ def rows8(rng, rows, K, spread=3):
 
 def mats8(rng, n, N, K):
     """Random codes of moderate size with block scales of very different sizes."""
-    q = F.encode(rng.standard_normal((n, N, K)) * 60.0)
+    v = torch.from_numpy(rng.standard_normal((n, N, K), dtype=np.float32) * np.float32(60.0))
+    q = v.to(FP8).view(torch.uint8).numpy()  # below 448 all of them
+    assert (q & 0x7F != 0x7F).all()
     s = (2.0 ** rng.uniform(-12, -6, (n, F.blocks(N), F.blocks(K)))).astype(np.float32)
     return q, s
 
 
 def prod_bound(K):
-    return (264 + F.blocks(K) + 10) * U
+    return (264 + F.blocks(K) + 2) * U
 
 
 def check_prod(got, want, mag, K, dt):
@@ -186,6 +188,8 @@ GEMM_CASES = [
     (1, 1, 16), (1, 2048, 4096), (2, 100, 128), (5, 136, 144), (7, 1000, 1424), (31, 129, 272), (33, 256, 1408),
     (64, 640, 512), (127, 128, 256), (128, 257, 384), (129, 384, 2048), (300, 1000, 1424), (257, 2050, 640),
     (1300, 4100, 272),   # 256-column tiles, ragged on both sides
+    (16, 200, 384), (16, 136, 640), (15, 72, 640),   # whole and short last stages of several K blocks
+    (700, 1600, 256), (700, 1602, 384),              # 128-column tiles, whole and odd sectors
 ]
 
 
@@ -222,6 +226,26 @@ def test_gemm_many_tiles_per_sm():
     pick = rng.permutation(rows)[:200]
     want, mag = F.gemm(a[pick], w)
     check_prod(out[dev(pick)], want, mag, K, F32)
+
+
+@pytest.mark.slow
+@pytest.mark.parametrize("rows,N,K", [(33000, 65536, 16), (1 << 21, 16, 1040)])
+def test_gemm_past_32_bit_offsets(rows, N, K):
+    """Outputs, and operands, of more than 2^31 values: the last rows are right."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    aq = torch.randint(0, 96, (rows, K), generator=g, dtype=torch.uint8, device="cuda")  # values up to 8
+    as_ = torch.rand(rows, F.blocks(K), generator=g, device="cuda") + 0.5
+    wq = torch.randint(0, 96, (N, K), generator=g, dtype=torch.uint8, device="cuda")
+    ws_ = torch.rand(F.blocks(N), F.blocks(K), generator=g, device="cuda") + 0.5
+    out = torch.empty(rows, N, dtype=BF16, device="cuda")
+    assert max(out.numel(), aq.numel()) > 2 ** 31
+    ws = make_ws()
+    moe.moe_gemm_fp8(aq, as_, wq, ws_, out, ws)
+    assert moe.moe_get_error(ws) == 0
+    pick = torch.tensor([0, 1, 127, 128, rows // 2, rows - 130, rows - 2, rows - 1], device="cuda")
+    a = F.dequant_rows(codes_np(aq[pick]), f64(as_[pick]))
+    want, mag = F.gemm(a, F.dequant_mats(codes_np(wq), f64(ws_)))
+    check_prod(out[pick], want, mag, K, BF16)
 
 
 def test_gemm_block_scales_and_order():
@@ -306,7 +330,7 @@ def test_grouped(T, k, E, N, K, skew, a_div, scatter, dt):
 
 
 def test_grouped_bucket_sizes_around_tiles():
-    counts = [0, 1, 127, 0, 128, 129, 3, 256, 31, 32, 33, 0]
+    counts = [0, 1, 127, 0, 128, 129, 3, 256, 31, 32, 33, 0, 63, 64, 65, 16, 17, 193]
     rng = np.random.default_rng(8)
     off, ent = routing(rng, 0, 1, len(counts), counts=counts)
     P, N, K = sum(counts), 200, 320
@@ -361,6 +385,8 @@ SWIGLU_CASES = [
     (300, 4, 16, 640, 384, -1),
     (300, 8, 1024, 128, 144, 1),
     (700, 2, 3, 272, 256, 0),
+    (3, 8, 64, 256, 272, -1),
+    (640, 3, 8, 1040, 384, -1),
 ]
 
 
