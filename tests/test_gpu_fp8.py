@@ -306,6 +306,7 @@ GROUP_CASES = [
     (200, 4, 16, 640, 384, 1.0),
     (300, 8, 1024, 128, 144, 0.5),
     (700, 2, 3, 2050, 256, 1.0),
+    (1100, 8, 1024, 272, 144, 0.1),   # as many experts as there may be, full tiles
 ]
 
 
@@ -387,6 +388,7 @@ SWIGLU_CASES = [
     (700, 2, 3, 272, 256, 0),
     (3, 8, 64, 256, 272, -1),
     (640, 3, 8, 1040, 384, -1),
+    (1100, 8, 1024, 144, 144, -1),
 ]
 
 
