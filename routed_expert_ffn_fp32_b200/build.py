@@ -1,4 +1,5 @@
-"""Build the CUDA library in-tree: routed_expert_ffn_fp32_b200/libmoe_b200.so.
+"""Build the CUDA library in-tree: routed_expert_ffn_fp32_b200/libmoe_b200.so,
+and _fp8_binding.so, the argument marshalling of the 8-bit operators' binding.
 
 nvcc -gencode arch=compute_100a,code=sm_100a (B200 only), one object per
 csrc/*.cu, linked into a shared library that exports the C ABI of
@@ -18,6 +19,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_b200.so")
+BINDING_SRC = os.path.join(CSRC, "moe_fp8_binding.cpp")
+BINDING = os.path.join(PKG, "_fp8_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVFLAGS = ["-O3", "-lineinfo", "-std=c++20", "--expt-relaxed-constexpr",
@@ -49,6 +52,21 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_cmd(out: str):
+    import sysconfig
+
+    import torch
+
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(_nvcc()))), "include")
+    dirs = [INCLUDE, os.path.join(home, "include"), os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            cuda, sysconfig.get_paths()["include"]]
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-w",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *[f for d in dirs for f in ("-isystem", d)], BINDING_SRC, "-o", out, "-L", os.path.join(home, "lib"),
+            "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     """Compile (incrementally) and return the path of the shared library."""
     os.makedirs(BUILD, exist_ok=True)
@@ -62,14 +80,16 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         objs.append(obj)
         if _stale(obj, [src, __file__] + headers):
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
+    if _stale(BINDING, [BINDING_SRC, __file__, os.path.join(INCLUDE, "moe.h")]):
+        jobs.append(_binding_cmd(BINDING))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
-        log = os.path.join(BUILD, os.path.basename(cmd[-1]) + ".log")
+        log = os.path.join(BUILD, os.path.basename(cmd[cmd.index("-o") + 1]) + ".log")
         with open(log, "w") as f:
             f.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
         if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed ({cmd[-3]}):\n{r.stderr[-6000:]}")
+            raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({cmd[cmd.index('-o') - 1]}):\n{r.stderr[-6000:]}")
         return r.stderr
 
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:

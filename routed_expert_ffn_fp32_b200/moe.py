@@ -370,10 +370,9 @@ def moe_decode_mxfp4(q, s, K, out, stream=None):
 
 # ------------------------------------------------------- 8-bit operators ---
 # E4M3 codes are torch.float8_e4m3fn or uint8 tensors.  Sizes come from the
-# tensors, so these wrappers check shapes and types as well; a mismatch raises
-# ValueError before anything is launched.  A decode step makes many of these
-# calls, so the checks are written to cost little: the wrapper, the launch
-# included, takes about as long as the smallest kernel.
+# tensors, so shapes and types are checked as well; a mismatch raises ValueError
+# before anything is launched.  A decode step makes many of these calls, so the
+# operators' own marshalling is compiled (csrc/moe_fp8_binding.cpp).
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _F32 = torch.float32
 
@@ -383,15 +382,23 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _b128(n):
-    return (n + 127) // 128
+_fp8 = None
 
 
-def _dtype_of(t, what):
-    code = MOE_DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{what}: expected bfloat16, float16 or float32, got {t.dtype}")
-    return code
+def _bind_fp8():
+    """The compiled marshalling of the 8-bit operators, bound to the library."""
+    global _fp8
+    if _fp8 is None:
+        lib = load_library()
+        try:
+            from . import _fp8_binding as ext
+        except ImportError as e:
+            raise RuntimeError("_fp8_binding.so is missing or does not fit this torch: build it with "
+                               "`python -m routed_expert_ffn_fp32_b200.build`") from e
+        ext.bind(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in
+                   ("moe_rmsnorm_quant_fp8", "moe_gemm_fp8", "moe_grouped_gemm_fp8", "moe_grouped_swiglu_fp8")))
+        _fp8 = ext
+    return _fp8
 
 
 def _ptrs(*ts):
@@ -456,34 +463,18 @@ def moe_rmsnorm_quant_fp8(x, weight, eps, q_out, s_out, residual=None, residual_
                           stream=None):
     """Residual addition, root-mean-square norm and E4M3 quantisation of the
     rows of x [rows, H] (moe.h).  residual_out, y_out may be None."""
-    dt = _dtype_of(x, "x")
-    shape = x.shape
-    rows, H = _rows8(q_out, s_out, "q_out, s_out")
-    if shape != (rows, H) or weight.shape != (H,) or weight.dtype is not _F32:
-        raise ValueError("expected x, q_out [rows, H] and a float32 weight [H]")
-    for t in (residual, residual_out, y_out):
-        if t is not None and (t.shape != shape or t.dtype is not x.dtype):
-            raise ValueError("residual, residual_out, y_out: expected the shape and type of x")
-    dev, (px, pr, pw, pro, py, pq, ps) = _ptrs(x, residual, weight, residual_out, y_out, q_out, s_out)
-    _call((_lib or load_library()).moe_rmsnorm_quant_fp8, "moe_rmsnorm_quant_fp8", dev, stream,
-          (px, pr, pw, rows, H, dt, eps, pro, py, pq, ps))
+    st = (_fp8 or _bind_fp8()).norm(x, weight, eps, q_out, s_out, residual, residual_out, y_out,
+                                    None if stream is None else _s(stream))
+    if st:
+        raise MoeError(st, "moe_rmsnorm_quant_fp8")
 
 
 def moe_gemm_fp8(a_q, a_s, w_q, w_s, out, ws, stream=None):
     """out [rows, N] = A [rows, K] times W [N, K] transposed, both E4M3 with
     scales per 128 (moe.h); out is bfloat16, float16 or float32."""
-    dt = _dtype_of(out, "out")
-    rows, K = _rows8(a_q, a_s, "a_q, a_s")
-    shape = w_q.shape
-    if len(shape) != 2 or shape[1] != K or w_q.dtype not in _CODES or w_s.dtype is not _F32 \
-            or w_s.shape != ((shape[0] + 127) // 128, (K + 127) // 128):
-        raise ValueError("w_q, w_s: expected codes [N, K] and float32 scales [ceil(N / 128), ceil(K / 128)]")
-    N = shape[0]
-    if out.shape != (rows, N):
-        raise ValueError("out: expected [rows, N]")
-    dev, (pa, pas, pw, pws, po, pk) = _ptrs(a_q, a_s, w_q, w_s, out, ws)
-    _call((_lib or load_library()).moe_gemm_fp8, "moe_gemm_fp8", dev, stream,
-          (pa, pas, pw, pws, rows, N, K, dt, po, pk, ws.nbytes))
+    st = (_fp8 or _bind_fp8()).gemm(a_q, a_s, w_q, w_s, out, ws, None if stream is None else _s(stream))
+    if st:
+        raise MoeError(st, "moe_gemm_fp8")
 
 
 def moe_grouped_gemm_fp8(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div=0, scatter=False,
@@ -491,35 +482,20 @@ def moe_grouped_gemm_fp8(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div=0,
     """Products grouped by expert (moe.h): out [n_pairs, N], w_q [E, N, K],
     offsets and entries from moe_bucket.  a_div = k takes token rows, 0 rows in
     bucket order; scatter writes row entries[p] instead of p."""
-    dt = _dtype_of(out, "out")
-    a_rows, K = _rows8(a_q, a_s, "a_q, a_s")
-    E, N, _ = _mats8(w_q, w_s, "w_q, w_s", K)
-    shape = out.shape
-    if len(shape) != 2 or shape[1] != N:
-        raise ValueError("out: expected [n_pairs, N]")
-    P = shape[0]
-    _groups(offsets, entries, E, P)
-    dev, (pa, pas, pw, pws, pf, pe, po, pk) = _ptrs(a_q, a_s, w_q, w_s, offsets, entries, out, ws)
-    _call((_lib or load_library()).moe_grouped_gemm_fp8, "moe_grouped_gemm_fp8", dev, stream,
-          (pa, pas, a_rows, pw, pws, pf, pe, P, E, N, K, a_div, scatter, dt, po, pk, ws.nbytes))
+    st = (_fp8 or _bind_fp8()).grouped(a_q, a_s, w_q, w_s, offsets, entries, out, ws, a_div, scatter,
+                                       None if stream is None else _s(stream))
+    if st:
+        raise MoeError(st, "moe_grouped_gemm_fp8")
 
 
 def moe_grouped_swiglu_fp8(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws,
                            a_div=0, stream=None):
     """Grouped gate / up projections with SwiGLU and E4M3 quantisation (moe.h):
     q_out [n_pairs, I], s_out [n_pairs, ceil(I / 128)] in bucket order."""
-    a_rows, H = _rows8(a_q, a_s, "a_q, a_s")
-    E, I, _ = shape = _mats8(gate_q, gate_s, "gate_q, gate_s", H)
-    if _mats8(up_q, up_s, "up_q, up_s", H) != shape:
-        raise ValueError("up_q: expected the shape of gate_q")
-    P, width = _rows8(q_out, s_out, "q_out, s_out")
-    if width != I:
-        raise ValueError("q_out: expected [n_pairs, I]")
-    _groups(offsets, entries, E, P)
-    dev, (pa, pas, pg, pgs, pu, pus, pf, pe, pq, ps, pk) = _ptrs(
-        a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws)
-    _call((_lib or load_library()).moe_grouped_swiglu_fp8, "moe_grouped_swiglu_fp8", dev, stream,
-          (pa, pas, a_rows, pg, pgs, pu, pus, pf, pe, P, E, I, H, a_div, pq, ps, pk, ws.nbytes))
+    st = (_fp8 or _bind_fp8()).swiglu(a_q, a_s, gate_q, gate_s, up_q, up_s, offsets, entries, q_out, s_out, ws,
+                                      a_div, None if stream is None else _s(stream))
+    if st:
+        raise MoeError(st, "moe_grouped_swiglu_fp8")
 
 
 @dataclasses.dataclass
