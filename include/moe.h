@@ -359,8 +359,9 @@ MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_
  * N in [1, 65536], rows up to 2^21, E up to 1024; pointers 16-byte aligned.
  * Zero rows are allowed and write nothing.  `ws` is a zeroed workspace
  * (moe_workspace_init) of at least MOE_FP8_STATUS_BYTES bytes that holds the
- * latched error and the wait limit (moe_get_error, moe_workspace_set_limits)
- * and no scratch: calls on different streams may share it unless stated
+ * latched error, the wait limit and the debug switch (moe_get_error,
+ * moe_workspace_set_limits; limits below 20 us count as 20; the switch holds
+ * back the first block's scales) and no scratch: calls on different streams may share it unless stated
  * otherwise.  Outputs must not overlap inputs unless stated otherwise.
  * ------------------------------------------------------------------------- */
 #define MOE_FP8_STATUS_BYTES 128

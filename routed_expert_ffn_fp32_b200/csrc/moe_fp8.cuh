@@ -115,13 +115,13 @@ __device__ __forceinline__ bool bar_try_cluster(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok != 0;
 }
-// What a role needs to give up a wait: the CTA's abort flag, the error words
-// and the limit.
+// What a role needs to give up a wait: the CTA's abort flag and the error words,
+// which hold the limit.
 struct WaitCtl {
   volatile int* abort_flag;
   int* err;
-  unsigned long long limit_ns;
 };
+constexpr unsigned long long kFp8GraceNs = 20000;  // the limit is not read before a wait lasts that long
 // Bounded wait of a whole warp; false if it gave up (or another role already
 // did).  Every lane asks, so the code around it stays warp-uniform.
 template <bool CLUSTER = false>
@@ -133,7 +133,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t bar, uint32_t parity, const Wa
   const unsigned long long t0 = global_ns();
   while (!try_once()) {
     if (__any_sync(kFull, *c.abort_flag != 0)) return false;
-    if (__any_sync(kFull, global_ns() - t0 > c.limit_ns)) {
+    const unsigned long long waited = global_ns() - t0;
+    bool over = false;
+    if (waited > kFp8GraceNs) {
+      const unsigned us = *(reinterpret_cast<const volatile unsigned*>(c.err) + 2);
+      over = waited > (us ? us : kDefaultWaitUs) * 1000ull;
+    }
+    if (__any_sync(kFull, over)) {
       *c.abort_flag = 1;
       if ((threadIdx.x & 31) == 0) latch_error(c.err, MOE_ERR_TIMEOUT, where);
       return false;

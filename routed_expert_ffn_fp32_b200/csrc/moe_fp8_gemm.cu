@@ -51,8 +51,6 @@
 namespace moe {
 namespace {
 
-constexpr unsigned long long kLimitNs = 2000000000ull;  // default bound of a wait: 2 s
-
 // SECTORS: the output's rows are whole 32-byte sectors (always with swiglu, or
 // MR = 16).
 template <bool SWIGLU, int BN, int MR, bool SECTORS>
@@ -329,67 +327,75 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
+  const int NT = (a.N + C::COLS - 1) / C::COLS;
+  if (a.offsets == nullptr && threadIdx.x == 0) {  // one group of all rows
+    t_off[0] = t_beg[0] = 0;
+    t_off[1] = (a.P + MR - 1) / MR * NT;
+    t_beg[1] = a.P;
+  }
+  tcgen_fence_before();
+  if (S > 1) cluster_barrier();  // the other CTAs' barriers exist before anyone arrives on them
+  else __syncthreads();
+  tcgen_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // everything above runs while the kernel before drains; from here on memory
+  // is read (a dense product goes straight to its copies)
   pdl_wait();
   pdl_trigger();
-  const unsigned wait_us = *(reinterpret_cast<const volatile unsigned*>(a.err) + 2);
-  const unsigned debug = *(reinterpret_cast<const volatile unsigned*>(a.err) + 3);
 
   // rows and tiles before every bucket: a thread takes PER neighbouring
   // buckets, warps scan their sums, and everyone adds the warps before its own.
   // Offsets that are not ascending inside [0, P] stop the whole call (latched,
   // nothing written).
-  const int NT = (a.N + C::COLS - 1) / C::COLS;
-  constexpr int PER = (kMaxExperts + kThreads - 1) / kThreads;
-  const int per = (a.E + kThreads - 1) / kThreads;
-  int beg[PER + 1], sum = 0, bad = 0;
+  if (a.offsets != nullptr) {
+    constexpr int PER = (kMaxExperts + kThreads - 1) / kThreads;
+    const int per = (a.E + kThreads - 1) / kThreads;
+    int beg[PER + 1], sum = 0, bad = 0;
 #pragma unroll
-  for (int j = 0; j <= PER; ++j) {
-    const int e = int(threadIdx.x) * per + j;
-    beg[j] = j <= per && e <= a.E ? (a.offsets ? a.offsets[e] : e * a.P) : 0;
-  }
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = int(threadIdx.x) * per + j;
-    if (j < per && e < a.E) {
-      bad |= beg[j] < 0 || beg[j + 1] < beg[j] || beg[j + 1] > a.P;
-      sum += (beg[j + 1] - beg[j] + MR - 1) / MR * NT;
+    for (int j = 0; j <= PER; ++j) {
+      const int e = int(threadIdx.x) * per + j;
+      beg[j] = j <= per && e <= a.E ? a.offsets[e] : 0;
     }
-  }
-  int inc = sum;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(kFull, inc, o);
-    if (lane >= o) inc += y;
-  }
-  if (lane == 31) s_part[warp] = inc;
-  tcgen_fence_before();
-  bad = __syncthreads_or(bad);
-  tcgen_fence_after();
-  if (bad && threadIdx.x == 0) latch_error(a.err, MOE_ERR_DEVICE_DATA, 500);
-  int run = inc - sum;
-  for (int w = 0; w < warp; ++w) run += s_part[w];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = int(threadIdx.x) * per + j;
-    if (j < per && e < a.E) {
-      t_off[e] = run;
-      t_beg[e] = beg[j];
-      run += (beg[j + 1] - beg[j] + MR - 1) / MR * NT;
-      if (e == a.E - 1) {
-        t_off[a.E] = bad ? 0 : run;
-        t_beg[a.E] = beg[j + 1];
+    for (int j = 0; j < PER; ++j) {
+      const int e = int(threadIdx.x) * per + j;
+      if (j < per && e < a.E) {
+        bad |= beg[j] < 0 || beg[j + 1] < beg[j] || beg[j + 1] > a.P;
+        sum += (beg[j + 1] - beg[j] + MR - 1) / MR * NT;
       }
     }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_part[warp] = inc;
+    bad = __syncthreads_or(bad);
+    if (bad && threadIdx.x == 0) latch_error(a.err, MOE_ERR_DEVICE_DATA, 500);
+    int run = inc - sum;
+    for (int w = 0; w < warp; ++w) run += s_part[w];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = int(threadIdx.x) * per + j;
+      if (j < per && e < a.E) {
+        t_off[e] = run;
+        t_beg[e] = beg[j];
+        run += (beg[j + 1] - beg[j] + MR - 1) / MR * NT;
+        if (e == a.E - 1) {
+          t_off[a.E] = bad ? 0 : run;
+          t_beg[a.E] = beg[j + 1];
+        }
+      }
+    }
+    __syncthreads();
   }
-  if (S > 1) cluster_barrier();  // the other CTAs' barriers exist before anyone arrives on them
-  else __syncthreads();
-  const uint32_t tmem = *tmem_slot;
   const int n_tiles = t_off[a.E];
   const int KB = fp8_blocks(a.K), KG = (KB + C::KU - 1) / C::KU;  // K blocks, stages of them
   const int first = blockIdx.x / S, step = gridDim.x / S;
   const bool gather = a.a_div > 0, scatter = a.scatter;
   const bool by_row = MR == 16 ? rows_by_four(a) : gather;
-  const WaitCtl ctl{abort_flag, a.err, wait_us ? wait_us * 1000ull : kLimitNs};
+  const WaitCtl ctl{abort_flag, a.err};
 
   // the end of every role.  (Each side of the register split calls it by itself
   // and returns: where the two meet again, ptxas holds both to the launch's
@@ -403,6 +409,14 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       tcgen_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM)
                    : "memory");
+    }
+  };
+
+  // After a give-up.  A stage's barrier may then lack another producer for good,
+  // so the copies in flight get a millisecond, far beyond any copy's time.
+  auto let_copies_land = [&] {
+    const unsigned long long t0 = global_ns();
+    while (global_ns() - t0 < 1000000ull) {
     }
   };
 
@@ -435,7 +449,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       // (a pair's gate and up rows alternate by K block, so it takes them singly)
       constexpr bool DEEP_W = C::KU > 1 && !SWIGLU;
       Ring<C::NS> ring;
-      uint32_t fills = 0, used = 0;
       uint64_t keep, once;
       asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
       asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
@@ -454,9 +467,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           if (!ok) break;
           const uint32_t w = smem_addr(smem + C::W0 + ring.stage * C::B_BYTES);
           const uint32_t fb = smem_addr(&full[ring.stage]);
-          // debug switch: the first stage gets no weights, so the MMA warp's
-          // bounded wait on it runs out
-          if ((debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0 && it == first && kg == 0) continue;
           if (elect_one()) {
             const int kn = min(C::KU, KB - kg * C::KU);
             if (DEEP_W && maps.deep) {  // blocks past K arrive as zeros
@@ -481,19 +491,9 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
               if (kg * C::KU + u < KB) gather_block(t, 1, r, st + u * C::A_BLK, (kg * C::KU + u) * 128, fb);
             __syncwarp();
           }
-          fills ^= 1u << ring.stage;
-          used |= 1u << ring.stage;
         }
       }
-      // after a give-up, let every copy that was requested land (bounded)
-      if (*abort_flag && lane == 0) {
-        for (int s = 0; s < C::NS; ++s) {
-          if (!((used >> s) & 1u)) continue;
-          const unsigned long long t0 = global_ns();
-          while (!bar_try(smem_addr(&full[s]), ((fills >> s) & 1u) ^ 1u) && global_ns() - t0 < 100000000ull) {
-          }
-        }
-      }
+      if (!ok || *abort_flag) let_copies_land();
     } else if (warp == kEpiWarps + 2) {
       // --------------------------------------------------------- row producer
       constexpr bool DEEP_A = C::KU > 1 && MR == C::ABOX;  // a block's rows are one box
@@ -536,13 +536,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           __syncwarp();
         }
       }
-      // after a give-up: a stage's barrier may lack another producer, so these
-      // copies are given a millisecond to land
-      if (!ok || *abort_flag) {
-        const unsigned long long t0 = global_ns();
-        while (global_ns() - t0 < 1000000ull) {
-        }
-      }
+      if (!ok || *abort_flag) let_copies_land();
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
       // lane l holds the rows of TMEM lanes l, l + 32, .. and both weight scales
@@ -552,6 +546,10 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       Ring<C::NS> ring;
       Ring<C::SLOTS> slot;
       const int NB = fp8_blocks(a.N);
+      // debug switch: the first stage's scales never arrive, so the bounded waits
+      // for it run out
+      const unsigned debug = *(reinterpret_cast<const volatile unsigned*>(a.err) + 3);
+      bool starve = (debug & MOE_DEBUG_STARVE_FIRST_WAIT) && blockIdx.x == 0;
       bool ok = true;
       for (int it = first; it < n_tiles && ok; it += step) {
         const Tile t = tile_of<MR>(t_off, t_beg, a.E, it);
@@ -607,12 +605,13 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
                 }
             }
             __syncwarp();
-            if (lane == 0) {
+            if (lane == 0 && !starve) {
               bar_arrive(smem_addr(&scl_full[slot.stage]));
               // the MMAs wait for this warp too: it must not fall a round of
               // the ring behind, where the empty barrier's parity repeats
               bar_arrive(smem_addr(&full[ring.stage]));
             }
+            starve = false;
             ring.next();
             slot.next();
           }
