@@ -2,8 +2,8 @@
 // types, devices and pointers out of the tensors, checks them against one
 // another and calls the C entry point (include/moe.h) on the current stream of
 // the tensors' device.  A decode step makes many of these calls and each is as
-// short as a launch; the same checks written in Python took 3 to 6 us of them
-// (dense product 7.8 us a call, 5.2 so).
+// short as a launch: 3.0 us for the norm or a dense product, 4.1 for the gate /
+// up pair (6.9 to 10.9 us with the same checks written in Python over ctypes).
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>

@@ -33,10 +33,10 @@
 // TMEM load and FMA is the longer one (TMEM loads alone cost nothing, half the
 // FMAs saves 10 us, the scales 10 us).  Grouped products of many experts are
 // bound by HBM: down, T = 5, k = 8, 256 experts, H = 4096, I = 2048: 53 us for
-// 316 MB (6.0 TB/s); T = 2048: 385 us (6.0 TB/s); gate / up T = 1: 26.3 us for
-// 134 MB (5.1 TB/s), T = 2048: 890 us (4.9 TB/s, TMA row gather and the tile's
+// 316 MB (6.0 TB/s); T = 2048: 380 us (6.1 TB/s); gate / up T = 1: 26.3 us for
+// 134 MB (5.1 TB/s), T = 2048: 850 us (5.1 TB/s, TMA row gather and the tile's
 // end beside the weights).  Under a sustained load the card's power limit lowers
-// the clock, and the full tiles follow it (163, 455 and 935 us).
+// the clock, and the full tiles follow it (162, 447 and 910 us).
 //
 // Few rows mean few tiles, so the tile gets narrower (down to 64 weight rows)
 // to spread the weights over more SMs; K is never split, so nothing has to be
