@@ -201,6 +201,10 @@ PyObject* grouped(PyObject*, PyObject* const* a, Py_ssize_t n) {
     groups(off, ent, E, P);
     const int32_t div = integer(a[8]);
     const int scatter = PyObject_IsTrue(a[9]);
+    if (scatter < 0) {
+      PyErr_Clear();
+      throw std::invalid_argument("scatter: expected a truth value");
+    }
     Call c;
     void *pa = c.ptr(aq), *pas = c.ptr(as), *pw = c.ptr(wq), *pws = c.ptr(wsc), *pf = c.ptr(off), *pe = c.ptr(ent),
          *po = c.ptr(out), *pk = c.ptr(ws);

@@ -405,18 +405,18 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     tcgen_fence_before();
     if (S > 1) cluster_barrier();  // no CTA leaves while another may write its maxima
     else __syncthreads();
+    if (*abort_flag) {
+      // Given up, and nobody issues copies any more.  A stage's barrier may lack
+      // a producer for good, so those in flight get a millisecond, far beyond
+      // any copy's time, before the CTA leaves its shared memory.
+      const unsigned long long t0 = global_ns();
+      while (global_ns() - t0 < 1000000ull) {
+      }
+    }
     if (warp == kEpiWarps + 1) {
       tcgen_fence_after();
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM)
                    : "memory");
-    }
-  };
-
-  // After a give-up.  A stage's barrier may then lack another producer for good,
-  // so the copies in flight get a millisecond, far beyond any copy's time.
-  auto let_copies_land = [&] {
-    const unsigned long long t0 = global_ns();
-    while (global_ns() - t0 < 1000000ull) {
     }
   };
 
@@ -493,7 +493,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           }
         }
       }
-      if (!ok || *abort_flag) let_copies_land();
     } else if (warp == kEpiWarps + 2) {
       // --------------------------------------------------------- row producer
       constexpr bool DEEP_A = C::KU > 1 && MR == C::ABOX;  // a block's rows are one box
@@ -536,7 +535,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           __syncwarp();
         }
       }
-      if (!ok || *abort_flag) let_copies_land();
     } else if (warp == kEpiWarps + 3) {
       // ------------------------------------------------------- scale producer
       // lane l holds the rows of TMEM lanes l, l + 32, .. and both weight scales
