@@ -353,7 +353,8 @@ MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_
  * product sums each block of 128 in the tensor core's float32 accumulator and
  * the blocks, times both scales, in float32, in ascending order.  Quantised outputs
  * take s = max(max|v| / 448, 2^-126) over a block's values that are not NaN,
- * and code = E4M3(v / s), rounded to nearest even; a NaN stays NaN.
+ * and code = E4M3(v / s): the quotient rounded to float32, then to E4M3, both to
+ * nearest even; a NaN stays NaN.
  *
  * K (and the width of quantised outputs) is a multiple of 16 in [16, 65536],
  * N in [1, 65536], rows up to 2^21, E up to 1024; pointers 16-byte aligned.

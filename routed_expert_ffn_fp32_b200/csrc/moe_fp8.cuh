@@ -26,8 +26,69 @@ __device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %2, %1;" : "=h"(r) : "f"(lo), "f"(hi));
   return r;
 }
-__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d) {
-  return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+// Two float32 operations in one instruction, each rounded as by itself.
+__device__ __forceinline__ unsigned long long pack2(float2 a) {
+  unsigned long long r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(unsigned long long a) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)));
+  return unpack2(r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack2(a)), "l"(pack2(b)), "l"(pack2(c)));
+  return unpack2(r);
+}
+
+// Quotients of a block's values by its scale s, as its codes need them: v * (1 /
+// s) is up to 1.5 units off, which next to a rounding border is the neighbouring
+// code.  The residual's correction (P. Markstein, "Computation of elementary
+// functions on the IBM RISC System/6000 processor", 1990) leaves it within 2^-22
+// units before the last rounding.  The quotients of float32 values that lie so
+// near to where the float32 next to a code's border begins are few enough to be
+// enumerated (tests/test_fp8_host.py), and all of them round as v / s does.  In
+// pairs it costs the norm 1 to 5 % (T = 4096, H = 4096: 27.1 -> 27.5 us; T = 777,
+// H = 7088: 7.2 -> 7.5) and gate / up nothing to speak of; the division itself
+// cost 10 to 35 % and 10 % (29.9, 9.5 us; T = 2048: 860 -> 945 us).
+struct Fp8Quotient {
+  float s, r;
+  // Brings scales whose residuals would leave float32's range to ones that do
+  // not, and the values with them.  An infinite scale: finite values give 0,
+  // infinite ones NaN.
+  template <int N>
+  __device__ __forceinline__ Fp8Quotient(float scale, float2 (&v)[N]) : s(scale) {
+    if (s < 0x1p-80f) {
+      s *= 0x1p64f;
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = mul2(v[i], make_float2(0x1p64f, 0x1p64f));
+    }
+    r = 1.f / s;
+    if (r == 0.f) s = 0.f;
+  }
+  // (product less value, times -r: a negative zero keeps its sign)
+  __device__ __forceinline__ float2 operator()(float2 v) const {
+    const float2 t = mul2(v, make_float2(r, r));
+    return fma2(fma2(t, make_float2(s, s), mul2(v, make_float2(-1.f, -1.f))), make_float2(-r, -r), t);
+  }
+};
+// Codes of N pairs of values over their scale, two pairs to a word
+template <int N>
+__device__ __forceinline__ void fp8_codes(float2 (&v)[N], float scale, uint32_t (&q)[(N + 1) / 2]) {
+  const Fp8Quotient of(scale, v);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 d = of(v[i]);
+    const uint32_t two = f32x2_to_e4m3x2(d.x, d.y);
+    q[i / 2] = i % 2 ? q[i / 2] | (two << 16) : two;
+  }
 }
 
 // ---------------------------------------------------------------- launchers ---

@@ -810,17 +810,19 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
               if (r >= t.nvalid) break;
               const int drow = __shfl_sync(kFull, dst, r);
               if (drow < 0) continue;
-              const float s = fp8_scale(amax[i]), inv = 1.f / s;
+              const float s = fp8_scale(amax[i]);
               if (lane == 0 && rank == 0) a.s_out[size_t(drow) * NB + t.nt] = s;
               if (n < a.N) {  // N is a multiple of 16
                 uint8_t* o = a.q_out + size_t(drow) * a.N + n;
-                if constexpr (CPL == 4)
-                  *reinterpret_cast<uint32_t*>(o) =
-                      f32x4_to_e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
-                else if constexpr (CPL == 2)
-                  *reinterpret_cast<uint16_t*>(o) = uint16_t(f32x2_to_e4m3x2(h[i][0] * inv, h[i][1] * inv));
-                else
-                  *o = uint8_t(f32x2_to_e4m3x2(h[i][0] * inv, 0.f));
+                float2 hp[(CPL + 1) / 2];
+#pragma unroll
+                for (int j = 0; j < (CPL + 1) / 2; ++j)
+                  hp[j] = make_float2(h[i][2 * j], 2 * j + 1 < CPL ? h[i][(2 * j + 1) % CPL] : 0.f);
+                uint32_t code[1];
+                fp8_codes(hp, s, code);
+                if constexpr (CPL == 4) *reinterpret_cast<uint32_t*>(o) = code[0];
+                else if constexpr (CPL == 2) *reinterpret_cast<uint16_t*>(o) = uint16_t(code[0]);
+                else *o = uint8_t(code[0]);
               }
             }
           } else {
@@ -899,17 +901,19 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
 #pragma unroll
         for (int k = 0; k < C::PARTS * S; ++k) amax = fmaxf(amax, x[k * MR + place]);
         if (dst >= 0 && n0 < a.N) {
-          const float s = fp8_scale(amax), inv = 1.f / s;
+          const float s = fp8_scale(amax);
           if (part == 0 && rank == 0) a.s_out[size_t(dst) * NB + nt] = s;
           uint8_t* o = a.q_out + size_t(dst) * a.N + n0;
-          auto code4 = [&](int j) {
-            return f32x4_to_e4m3x4(v[2 * j].x * inv, v[2 * j].y * inv, v[2 * j + 1].x * inv, v[2 * j + 1].y * inv);
-          };
 #pragma unroll
           for (int j = 0; j < HP / 16; ++j)
-            if (n0 + 16 * j < a.N)  // N is a multiple of 16
-              *reinterpret_cast<uint4*>(o + 16 * j) =
-                  make_uint4(code4(4 * j), code4(4 * j + 1), code4(4 * j + 2), code4(4 * j + 3));
+            if (n0 + 16 * j < a.N) {  // N is a multiple of 16
+              float2 h[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) h[i] = v[8 * j + i];
+              uint32_t code[4];
+              fp8_codes(h, s, code);
+              *reinterpret_cast<uint4*>(o + 16 * j) = make_uint4(code[0], code[1], code[2], code[3]);
+            }
         }
       } else if (work) {
         const int n0 = nt * BN + part * C::CP;

@@ -2,6 +2,7 @@
 entry points' refusals and the binding's (no GPU: every call returns or raises
 before anything is launched)."""
 import ctypes
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -184,3 +185,48 @@ def test_binding_calls_on_the_tensors_device(monkeypatch):
     moe._call(fn, "x", 1, None, (7,))
     moe._call(fn, "x", 0, None, (8,))
     assert seen == [(1, (7, 101)), (0, (8, 100))] and current == [0]
+
+
+def _rounded(x):
+    """The nearest number of 24 significant bits, ties to even (no range limits)."""
+    if x == 0:
+        return x
+    e = abs(x.numerator).bit_length() - x.denominator.bit_length()
+    e -= Fraction(2) ** e > abs(x)
+    unit = Fraction(2) ** (e - 23)
+    return round(x / unit) * unit
+
+
+def test_corrected_quotients_round_as_the_division():
+    """The kernels' quotient: t = v r with r = 1 / s, then t - (t s - v) r, each
+    step rounded to float32.  Before its last rounding it is within 2.5 * 2^-24
+    units of v / s: t is within 1.5 (r's half unit counts below one, t's own half),
+    the correction takes r's relative error of 2^-24 of that and at most another
+    2^-24 from the residual's rounding.  A code changes only where the rounded
+    quotient crosses a border of five significant bits, that is, where v / s lies
+    that near to the middle between the border and the next float32: for v, s
+    as 24-bit whole numbers A, S and the middle m, where |A 2^k - m S| is a few
+    units.  As m is next to a multiple of 2^20, S has to be as well; all such S, m
+    and A are gone through (and quotients at random)."""
+    def check(A, S):
+        r = _rounded(Fraction(1, S))
+        t = _rounded(A * r)
+        assert _rounded(t - _rounded(t * S - A) * r) == _rounded(Fraction(A, S)), (A, S)
+
+    found = 0
+    for S in (c * 2 ** 20 + d for c in range(8, 17) for d in range(-24, 25)):
+        if not 2 ** 23 <= S < 2 ** 24:
+            continue
+        for border in range(16, 32):
+            for finer in (20, 21, 22):        # below a power of two the next float32 is nearer
+                for side in (-1, 1):
+                    m = border * 2 ** finer + side
+                    for j in range(-24, 25):
+                        k = (m * S + j).bit_length() - 24
+                        if (m * S + j) % 2 ** k == 0:
+                            check((m * S + j) >> k, S)
+                            found += 1
+    assert found > 500
+    rng = np.random.default_rng(0)
+    for A, S in rng.integers(2 ** 23, 2 ** 24, (4000, 2)):
+        check(int(A), int(S))

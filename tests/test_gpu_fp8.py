@@ -645,3 +645,80 @@ def test_layer_norm_route_experts_combine(T, shared):
     np.testing.assert_array_equal(bits_np(out), first)
     np.testing.assert_array_equal(codes_np(q), first_q)
     assert moe.moe_get_error(ws) == 0
+
+
+# ------------------------------------------------- codes at rounding borders ---
+def around_borders(rng, n, top):
+    """n float32 values of a block whose largest is `top`: `top` first, then
+    values within two units of the middle between neighbouring codes, times the
+    block's scale, in the upper half of the range."""
+    s = np.float32(top) / np.float32(F.MAX)
+    mags = F.decode(np.arange(127))
+    mid = (mags[1:] + mags[:-1]) / 2
+    mid = mid[(mid > 226) & (mid < 440)]
+    v = (rng.choice(mid, n) * np.float64(s)).astype(np.float32)
+    for _ in range(2):
+        way = rng.integers(-1, 2, n)
+        v = np.where(way == 0, v, np.nextafter(v, np.where(way < 0, 0, np.inf).astype(np.float32)))
+    v[0] = top
+    return v
+
+
+def quotient_codes(v):
+    """Codes and scales of float32 rows as the header defines them: float32
+    quotients, rounded to E4M3."""
+    blocks = np.abs(v).reshape(v.shape[0], -1, 128).max(axis=2)
+    s = np.maximum(blocks / np.float32(F.MAX), np.float32(F.MIN_SCALE))
+    assert s.dtype == np.float32 and v.dtype == np.float32
+    return F.encode(v / np.repeat(s, 128, axis=1)), s
+
+
+def test_norm_codes_are_rounded_quotients():
+    """Rows of +-1 with eps = 0 have norm 1, so n is the weight exactly."""
+    rng = np.random.default_rng(21)
+    H = 16384
+    for _ in range(4):
+        w = np.concatenate([around_borders(rng, 128, rng.uniform(1, 2) * 2.0 ** rng.integers(-115, 120))
+                            for _ in range(H // 128)]).astype(np.float32)
+        w[5::128] = 0.0                          # the sign of a zero stays
+        sign = rng.choice(np.array([-1, 1], np.float32), (3, H))
+        q, s, _, y = run_norm(dev(sign), None, dev(w), F32, eps=0.0)
+        n = sign * w
+        np.testing.assert_array_equal(y.cpu().numpy(), n)
+        want_q, want_s = quotient_codes(n)
+        np.testing.assert_array_equal(s.cpu().numpy(), want_s)
+        np.testing.assert_array_equal(codes_np(q), want_q)
+
+
+@pytest.mark.parametrize("rows,blocks", [(3, 16), (3, 60), (3, 100), (40, 16), (150, 18), (150, 37), (150, 80)])
+def test_swiglu_codes_are_rounded_quotients(rows, blocks):
+    """Gates of 32, whose silu is 32 exactly, and ups put together from six
+    K blocks of four bits each, so h = 32 u exactly.  The column blocks run over
+    clusters of 4, 2 and 1 on each side of the tile heights."""
+    rng = np.random.default_rng(rows + blocks)
+    I, H = 128 * blocks, 7 * 128
+    u = np.stack([around_borders(rng, 128, np.float32(2 ** 24 - rng.integers(1, 2 ** 15))) for _ in range(blocks)])
+    u = u.reshape(-1).astype(np.int64)
+    assert (u >= 2 ** 23).all() and (u < 2 ** 24).all()   # 24-bit whole numbers, each a float32
+    uq, gq = np.zeros((1, I, H)), np.zeros((1, I, H))
+    gq[0, :, 0] = 32.0
+    us = np.ones((1, blocks, 7), np.float32)
+    for b in range(6):
+        uq[0, :, 128 * (b + 1)] = (u >> (20 - 4 * b)) & 15
+        us[0, :, b + 1] = 2.0 ** -(4 * b)
+    gs = np.ones((1, blocks, 7), np.float32)
+    aq = np.zeros((rows, H))
+    aq[:, ::128] = 1.0
+    power = rng.integers(-3, 4, rows)           # rows at their own power of two
+    as_ = np.ones((rows, 7), np.float32)
+    as_[:, 1:] = 2.0 ** power[:, None]
+    q = torch.empty(rows, I, dtype=torch.uint8, device="cuda")
+    s = torch.empty(rows, blocks, device="cuda")
+    ws = make_ws()
+    moe.moe_grouped_swiglu_fp8(*(dev(t) for t in (F.encode(aq), as_, F.encode(gq), gs, F.encode(uq), us)), None, None,
+                               q, s, ws)
+    assert moe.moe_get_error(ws) == 0
+    h = (32.0 * u[None] * 2.0 ** -20 * 2.0 ** power[:, None]).astype(np.float32)
+    want_q, want_s = quotient_codes(h)
+    np.testing.assert_array_equal(s.cpu().numpy(), want_s)
+    np.testing.assert_array_equal(codes_np(q), want_q)
