@@ -513,15 +513,19 @@ class Fp8Experts:
     def n_experts(self) -> int:
         return int(self.gate_q.shape[0])
 
-    def cstruct(self) -> moe_fp8_experts_t:
+    def tensors(self):
+        return self.gate_q, self.gate_s, self.up_q, self.up_s, self.down_q, self.down_s
+
+    def cstruct(self, ptrs=None) -> moe_fp8_experts_t:
+        """Checks the shapes; ``ptrs``: the tensors' addresses, where the caller
+        has them already."""
         _, I, H = self.gate_q.shape
         _mats8(self.gate_q, self.gate_s, "gate", H)
         _mats8(self.up_q, self.up_s, "up", H)
         _mats8(self.down_q, self.down_s, "down", I)
         _need(self.up_q.shape == self.gate_q.shape and self.down_q.shape == (self.n_experts, H, I),
               "expected gate, up [n, I, H] and down [n, H, I]")
-        return moe_fp8_experts_t(_p(self.gate_q), _p(self.gate_s), _p(self.up_q), _p(self.up_s),
-                                 _p(self.down_q), _p(self.down_s), self.n_experts)
+        return moe_fp8_experts_t(*(ptrs or map(_p, self.tensors())), self.n_experts)
 
 
 def fp8_workspace(shape: moe_shape_t, has_shared: bool = False, device="cuda", stream=None) -> torch.Tensor:
@@ -545,9 +549,12 @@ def moe_expert_ffn_fp8(experts: Fp8Experts, shared, x_q, x_s, offsets, entries, 
     rows = shape.T * (shape.k + (shared is not None))
     _need(partial_out.dtype == torch.float32 and partial_out.shape == (rows, shape.H),
           "partial_out: expected float32 [T k (+ T), H]")
-    dev, (px, pxs, pf, pe, po, pk, _) = _ptrs(x_q, x_s, offsets, entries, partial_out, ws, experts.gate_q)
+    dev, (px, pxs, pf, pe, po, pk, *mats) = _ptrs(x_q, x_s, offsets, entries, partial_out, ws, *experts.tensors(),
+                                                  *(shared.tensors() if shared is not None else ()))
+    ex = experts.cstruct(mats[:6])
+    sh = None if shared is None else ctypes.byref(shared.cstruct(mats[6:]))
     _call(load_library().moe_expert_ffn_fp8, "moe_expert_ffn_fp8", dev, stream,
-          (_ex(experts), _ex(shared), px, pxs, pf, pe, shape, po, pk, ws.nbytes))
+          (ctypes.byref(ex), sh, px, pxs, pf, pe, shape, po, pk, ws.nbytes))
 
 
 def moe_get_error(ws, stream=None) -> int:

@@ -230,3 +230,50 @@ def test_corrected_quotients_round_as_the_division():
     rng = np.random.default_rng(0)
     for A, S in rng.integers(2 ** 23, 2 ** 24, (4000, 2)):
         check(int(A), int(S))
+
+
+class _Faked(torch.Tensor):
+    """A host tensor that says it lies on a CUDA device."""
+    is_cuda = property(lambda self: True)
+
+    def get_device(self):
+        return self.on
+
+    @property
+    def device(self):
+        return torch.device("cuda", self.on)
+
+
+def _on(d, *shape, dtype=torch.uint8):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(_Faked)
+    t.on = d
+    return t
+
+
+def test_expert_ffn_refuses_tensors_of_several_devices(monkeypatch, lib):
+    f32, i32 = torch.float32, torch.int32
+    T, H, I, E, k = 4, 256, 128, 8, 2
+    calls = []
+    monkeypatch.setattr(moe, "_call", lambda fn, where, dev, stream, args: calls.append(dev))
+
+    def experts(n, d=1):
+        return moe.Fp8Experts(_on(d, n, I, H), _on(d, n, 1, 2, dtype=f32), _on(d, n, I, H), _on(d, n, 1, 2, dtype=f32),
+                              _on(d, n, H, I), _on(d, n, 2, 1, dtype=f32))
+
+    def call(ex, sh, **kw):
+        a = dict(x_q=_on(1, T, H), x_s=_on(1, T, 2, dtype=f32), offsets=_on(1, E + 1, dtype=i32),
+                 entries=_on(1, T * k, dtype=i32), partial_out=_on(1, T * (k + 1), H, dtype=f32), ws=_on(1, 1 << 16)) | kw
+        moe.moe_expert_ffn_fp8(ex, sh, shape=moe.shape_of(T, H, I, E, k), **a)
+
+    call(experts(E), experts(1))
+    assert calls == [1]
+    for which in (0, 1):
+        for field in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s"):
+            pair = [experts(E), experts(1)]
+            setattr(pair[which], field, getattr(experts((E, 1)[which], 0), field))
+            with pytest.raises(ValueError, match="one device"):
+                call(*pair)
+    for name, t in [("x_s", _on(0, T, 2, dtype=f32)), ("ws", _on(2, 1 << 16))]:
+        with pytest.raises(ValueError, match="one device"):
+            call(experts(E), experts(1), **{name: t})
+    assert calls == [1]
