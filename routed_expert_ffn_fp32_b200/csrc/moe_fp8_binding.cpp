@@ -48,7 +48,8 @@ const at::Tensor& tensor(PyObject* o) {
 
 int64_t b128(int64_t n) { return (n + 127) / 128; }
 int32_t i32(int64_t v) {
-  need(v <= std::numeric_limits<int32_t>::max(), "expected sizes below 2^31");
+  need(v >= std::numeric_limits<int32_t>::min() && v <= std::numeric_limits<int32_t>::max(),
+       "expected sizes and integers below 2^31");
   return int32_t(v);
 }
 bool codes(const at::Tensor& q) { return q.scalar_type() == at::kFloat8_e4m3fn || q.scalar_type() == at::kByte; }

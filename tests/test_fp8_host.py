@@ -277,3 +277,19 @@ def test_expert_ffn_refuses_tensors_of_several_devices(monkeypatch, lib):
         with pytest.raises(ValueError, match="one device"):
             call(experts(E), experts(1), **{name: t})
     assert calls == [1]
+
+
+def test_binding_refuses_integers_past_32_bits():
+    """A group width that wraps into range is not taken for one that is."""
+    f32, i32 = torch.float32, torch.int32
+    aq, as_ = _t(4, 272), _t(4, 3, dtype=f32)
+    off, ent, ws = _t(3, dtype=i32), _t(4, dtype=i32), _t(256)
+    mq, ms = _t(2, 128, 272), _t(2, 1, 3, dtype=f32)
+    for div in (1 << 31, 1 << 40, -(1 << 31) - 1, -(1 << 32) + 1, -(1 << 40)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            moe.moe_grouped_gemm_fp8(aq, as_, mq, ms, off, ent, _t(4, 128, dtype=f32), ws, a_div=div)
+        with pytest.raises(ValueError, match="2\\^31"):
+            moe.moe_grouped_swiglu_fp8(aq, as_, mq, ms, mq, ms, off, ent, _t(4, 128), _t(4, 1, dtype=f32), ws, a_div=div)
+    for div in (1 << 70, -(1 << 70), 1.5, "2"):
+        with pytest.raises(TypeError, match="integer"):
+            moe.moe_grouped_gemm_fp8(aq, as_, mq, ms, off, ent, _t(4, 128, dtype=f32), ws, a_div=div)
