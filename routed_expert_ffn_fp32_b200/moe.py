@@ -165,6 +165,18 @@ def _check(status: int, where: str):
         raise MoeError(status, where)
 
 
+def _status(fn, dev, stream, args) -> int:
+    """fn(*args, stream) on the tensors' device, made current when it is not."""
+    if dev != torch._C._cuda_getDevice():
+        with torch.cuda.device(dev):
+            return _status(fn, dev, stream, args)
+    return fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream))
+
+
+def _call(fn, where, dev, stream, args):
+    _check(_status(fn, dev, stream, args), where)
+
+
 def status_string(status: int) -> str:
     return load_library().moe_status_string(status).decode()
 
@@ -212,8 +224,11 @@ def moe_workspace_bytes(shape: moe_shape_t, path: int = MOE_PATH_AUTO,
 
 
 def moe_workspace_init(ws: torch.Tensor, stream=None):
-    _check(load_library().moe_workspace_init(_p(ws), ws.numel() * ws.element_size(), _s(stream)),
-           "moe_workspace_init")
+    """Zeroes a workspace.  Like the error and limit calls below it runs on the
+    workspace's device, by default on that device's current stream."""
+    p = _p(ws)
+    _call(load_library().moe_workspace_init, "moe_workspace_init", ws.get_device(), stream,
+          (p, ws.numel() * ws.element_size()))
 
 
 def make_workspace(shape: moe_shape_t, path=MOE_PATH_AUTO, precision=MOE_ACT_EXACT,
@@ -421,17 +436,6 @@ def _ptrs(*ts):
     return dev, out
 
 
-def _call(fn, where, dev, stream, args):
-    """fn(*args, stream) on the tensors' device, made current when it is not."""
-    if dev != torch._C._cuda_getDevice():
-        with torch.cuda.device(dev):
-            return _call(fn, where, dev, stream, args)
-    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _s(stream)
-    status = fn(*args, st)
-    if status != MOE_OK:
-        raise MoeError(status, where)
-
-
 def _rows8(q, s, what):
     """Checks codes [rows, K] and their scales; returns (rows, K)."""
     if q.dtype not in _CODES or s.dtype is not _F32:
@@ -558,7 +562,8 @@ def moe_expert_ffn_fp8(experts: Fp8Experts, shared, x_q, x_s, offsets, entries, 
 
 
 def moe_get_error(ws, stream=None) -> int:
-    return int(load_library().moe_get_error(_p(ws), _s(stream)))
+    p = _p(ws)
+    return int(_status(load_library().moe_get_error, ws.get_device(), stream, (p,)))
 
 
 def moe_get_error_static(stream=None) -> int:
@@ -566,8 +571,9 @@ def moe_get_error_static(stream=None) -> int:
 
 
 def moe_workspace_set_limits(ws, wait_us: int = 0, debug: int = 0, stream=None):
-    _check(load_library().moe_workspace_set_limits(_p(ws), wait_us, debug, _s(stream)),
-           "moe_workspace_set_limits")
+    p = _p(ws)
+    _call(load_library().moe_workspace_set_limits, "moe_workspace_set_limits", ws.get_device(), stream,
+          (p, wait_us, debug))
 
 
 def moe_version() -> str:

@@ -293,3 +293,47 @@ def test_binding_refuses_integers_past_32_bits():
     for div in (1 << 70, -(1 << 70), 1.5, "2"):
         with pytest.raises(TypeError, match="integer"):
             moe.moe_grouped_gemm_fp8(aq, as_, mq, ms, off, ent, _t(4, 128, dtype=f32), ws, a_div=div)
+
+
+def test_workspace_calls_run_on_the_workspaces_device(monkeypatch):
+    """Zeroing a workspace, setting its limits and reading its error are ordered
+    with the calls that use it: on its device's current stream, with that device
+    current, whatever device the caller is on."""
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, d):
+            self.d = d
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    class Stream:
+        cuda_stream = property(lambda self: 100 + current[0])
+
+    class Lib:
+        def __getattr__(self, name):
+            def fn(*args):
+                seen.append((name, current[0], args[-1]))
+                return moe.MOE_OK
+            return fn
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 100 + d, raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    monkeypatch.setattr(moe, "load_library", Lib)
+    for d in (0, 1):
+        ws = _on(d, 256)
+        for stream, want in ((None, 100 + d), (7, 7)):
+            seen.clear()
+            moe.moe_workspace_init(ws, stream)
+            moe.moe_workspace_set_limits(ws, 1000, 0, stream)
+            assert moe.moe_get_error(ws, stream) == 0
+            assert seen == [(n, d, want) for n in ("moe_workspace_init", "moe_workspace_set_limits", "moe_get_error")]
+            assert current == [0]
+    with pytest.raises(ValueError, match="CUDA"):
+        moe.moe_get_error(_t(256))
