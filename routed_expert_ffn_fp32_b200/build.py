@@ -67,6 +67,27 @@ def _binding_cmd(out: str):
             "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
 
 
+def _binding_env() -> str:
+    """What a built binding fits, beside its sources."""
+    import torch
+
+    return f"torch {torch.__version__}, Python {sys.version}"
+
+
+def _binding_stamp() -> str:
+    return os.path.join(BUILD, "_fp8_binding.env")
+
+
+def _binding_stale() -> bool:
+    if _stale(BINDING, [BINDING_SRC, __file__, os.path.join(INCLUDE, "moe.h")]):
+        return True
+    try:
+        with open(_binding_stamp()) as f:
+            return f.read() != _binding_env()
+    except OSError:
+        return True
+
+
 def build(verbose: bool = False, extra_flags=None) -> str:
     """Compile (incrementally) and return the path of the shared library."""
     os.makedirs(BUILD, exist_ok=True)
@@ -80,8 +101,6 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         objs.append(obj)
         if _stale(obj, [src, __file__] + headers):
             jobs.append([nvcc, *ARCH, *flags, "-c", src, "-o", obj])
-    if _stale(BINDING, [BINDING_SRC, __file__, os.path.join(INCLUDE, "moe.h")]):
-        jobs.append(_binding_cmd(BINDING))
 
     def run(cmd):
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -92,7 +111,15 @@ def build(verbose: bool = False, extra_flags=None) -> str:
             raise RuntimeError(f"{os.path.basename(cmd[0])} failed ({cmd[cmd.index('-o') - 1]}):\n{r.stderr[-6000:]}")
         return r.stderr
 
+    def binding():
+        env = _binding_env()
+        out = run(_binding_cmd(BINDING))
+        with open(_binding_stamp(), "w") as f:
+            f.write(env)
+        return out
+
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
+        beside = ex.submit(binding) if _binding_stale() else None
         for out in ex.map(run, jobs):
             if verbose:
                 sys.stderr.write(out)
@@ -101,6 +128,14 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode != 0:
             raise RuntimeError(f"link failed:\n{r.stderr[-4000:]}")
+    # last: the library and its C ABI need neither torch's headers nor Python's
+    if beside is not None:
+        try:
+            out = beside.result()
+        except Exception as e:
+            raise RuntimeError(f"{LIB} is built, the Python binding of its 8-bit operators is not: {e}") from e
+        if verbose:
+            sys.stderr.write(out)
     return LIB
 
 

@@ -337,3 +337,49 @@ def test_workspace_calls_run_on_the_workspaces_device(monkeypatch):
             assert current == [0]
     with pytest.raises(ValueError, match="CUDA"):
         moe.moe_get_error(_t(256))
+
+
+class _Compilers:
+    """Stands in for subprocess.run: records the commands, fails those that
+    `broken` picks."""
+
+    def __init__(self, monkeypatch, tmp_path):
+        self.ran, self.broken = [], lambda cmd: False
+        monkeypatch.setattr(build, "BUILD", str(tmp_path / "_build"))
+        monkeypatch.setattr(build.subprocess, "run", self)
+
+    def __call__(self, cmd, **kw):
+        self.ran.append(cmd)
+        return build.subprocess.CompletedProcess(cmd, int(self.broken(cmd)), "", "")
+
+    def build(self):
+        self.ran.clear()
+        build.build()
+        return [c for c in self.ran if build.BINDING in c]
+
+
+def test_binding_is_rebuilt_for_another_torch_or_python(lib, monkeypatch, tmp_path):
+    c = _Compilers(monkeypatch, tmp_path)
+    c.build()
+    assert c.build() == []
+    monkeypatch.setattr(torch, "__version__", torch.__version__ + ".other")
+    assert len(c.build()) == 1
+    assert c.build() == []
+    monkeypatch.setattr(build.sys, "version", "another Python")
+    assert len(c.build()) == 1
+    c.broken = lambda cmd: build.BINDING in cmd
+    monkeypatch.setattr(torch, "__version__", "a third")
+    for _ in range(2):  # a build that failed is not taken for done
+        with pytest.raises(RuntimeError):
+            c.build()
+
+
+def test_library_is_built_where_the_binding_cannot_be(lib, monkeypatch, tmp_path):
+    """The C ABI needs no torch headers."""
+    c = _Compilers(monkeypatch, tmp_path)
+    c.broken = lambda cmd: build.BINDING in cmd
+    monkeypatch.setattr(torch, "__version__", "other")
+    monkeypatch.setattr(build, "_stale", lambda target, deps: True)
+    with pytest.raises(RuntimeError, match="binding"):
+        c.build()
+    assert any(cmd[cmd.index("-o") + 1] == build.LIB for cmd in c.ran)
