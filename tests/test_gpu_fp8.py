@@ -722,3 +722,33 @@ def test_swiglu_codes_are_rounded_quotients(rows, blocks):
     want_q, want_s = quotient_codes(h)
     np.testing.assert_array_equal(s.cpu().numpy(), want_s)
     np.testing.assert_array_equal(codes_np(q), want_q)
+
+
+@pytest.mark.parametrize("rows", [3, 40, 150])
+def test_swiglu_silu_over_the_range(rows):
+    """silu against 64 bits through the block maxima: one column of every block
+    has a gate, exactly known (code 1 times a scale and a power of two), and an
+    up of 2^20, so s 448 = |silu(g)| 2^20.  Within 16 units of 2^-24 in all, two
+    of them for the scale's division and this test's own product."""
+    rng = np.random.default_rng(rows)
+    blocks, H = 400, 128
+    g = np.concatenate([np.linspace(-88, 88, 340), 10.0 ** rng.uniform(-6, 0, 60) * rng.choice([-1, 1], 60)])
+    gs = np.abs(g).astype(np.float32).reshape(1, blocks, 1)
+    gq, uq = np.zeros((1, blocks * 128, H)), np.zeros((1, blocks * 128, H))
+    at = np.arange(blocks) * 128 + rng.integers(0, 128, blocks)
+    gq[0, at, 5] = np.sign(g)
+    uq[0, at, 5] = 1.0
+    us = np.full((1, blocks, 1), 2.0 ** 20, np.float32)
+    aq = np.zeros((rows, H))
+    aq[:, 5] = 1.0
+    down = 2.0 ** -(np.arange(rows) % 5)        # the row's own power of two, in gate and up
+    q = torch.empty(rows, blocks * 128, dtype=torch.uint8, device="cuda")
+    s = torch.empty(rows, blocks, device="cuda")
+    ws = make_ws()
+    moe.moe_grouped_swiglu_fp8(*(dev(t) for t in (F.encode(aq), down[:, None].astype(np.float32), F.encode(gq), gs,
+                                                  F.encode(uq), us)), None, None, q, s, ws)
+    assert moe.moe_get_error(ws) == 0
+    gate = (np.sign(g) * gs.reshape(-1).astype(np.float64))[None] * down[:, None]
+    want = np.abs(F.silu(gate)) * 2.0 ** 20 * down[:, None]
+    err = np.abs(f64(s) * F.MAX / want - 1)
+    assert err.max() <= 16 * U, (float(err.max() / U), float(gate.reshape(-1)[err.argmax()]))
