@@ -75,7 +75,10 @@ struct Cfg {
   static constexpr int BUFS = BN * KU >= 256 ? 2 : 4;
   static constexpr int TMEM = BN * KU * BUFS;
   static constexpr int PROMOTERS = MR == 16 ? 2 : EW;
-  static constexpr int XCH_BYTES = SWIGLU ? 2 * PARTS * S * MR * 4 : 0;  // [2][PARTS S][MR] maxima
+  // Row maxima of a block's parts: [PARTS S][MR] (MR = 16: [S][MR], none alone).
+  // A cluster has one tile; a CTA by itself has many, and two buffers for them.
+  static constexpr int XCH = MR == 16 ? (S > 1 ? S * MR : 0) : PARTS * S * MR;  // floats
+  static constexpr int XCH_BYTES = SWIGLU ? (S > 1 ? 1 : 2) * XCH * 4 : 0;
   // MR = 16: a tile's sums.  Otherwise per lane the values of a store round
   // (without SECTORS), then its output row and the tile's column block.
   static constexpr int PC = BN == 256 ? 8 : 16;
@@ -93,8 +96,8 @@ struct Cfg {
   // weight stages, never out of them
   static constexpr int W0 = NS * A_BYTES;
   static constexpr int STG = NS * (A_BYTES + B_BYTES);
-  static constexpr int XCH = STG + STG_BYTES;
-  static constexpr int SCL = XCH + XCH_BYTES;
+  static constexpr int XCH0 = STG + STG_BYTES;
+  static constexpr int SCL = XCH0 + XCH_BYTES;
   static constexpr int CTL = SCL + SLOTS * KU * SLOT * 4; // barriers and flags
   static constexpr int CTL_BYTES = ((2 * NS + 2 * BUFS + SLOTS + 4) * 8 + 4 * (2 + THREADS / 32) + 15) / 16 * 16;
   static constexpr int TAB = CTL + CTL_BYTES;        // int [2][E + 1]: tiles and rows before e
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
   uint64_t* stg_empty = stg_full + 1;          // and have been stored
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(stg_empty + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* xch = reinterpret_cast<float*>(smem + C::XCH);
+  float* xch = reinterpret_cast<float*>(smem + C::XCH0);
   float* scl = reinterpret_cast<float*>(smem + C::SCL);
   int* s_part = const_cast<int*>(abort_flag) + 1;  // [warps]
   int* t_off = reinterpret_cast<int*>(smem + C::TAB);
@@ -777,24 +780,22 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
               for (int o = 16; o > 0; o >>= 1) amax[i] = fmaxf(amax[i], __shfl_xor_sync(kFull, amax[i], o));
             }
             if constexpr (S > 1) {
-              // the block's other columns are in the cluster's other CTAs.  Two
-              // exchange buffers: who writes one again has seen everyone arrive
-              // for the other, and they arrive after their reads.
-              float* x = xch + (local & 1u) * (S * MR);
+              // the block's other columns are in the cluster's other CTAs (and
+              // this is its one tile)
               if (lane < S) {
 #pragma unroll
                 for (int i = 0; i < HR; ++i)
                   if (hw + 6 * i < t.nvalid)
-                    cluster_st(cluster_map(smem_addr(x + rank * MR + hw + 6 * i), lane), amax[i]);
+                    cluster_st(cluster_map(smem_addr(xch + rank * MR + hw + 6 * i), lane), amax[i]);
                 cluster_arrive(cluster_map(smem_addr(xbar), lane));
               }
               __syncwarp();
-              if (!bar_wait<true>(smem_addr(xbar), local & 1u, ctl, 540)) break;
+              if (!bar_wait<true>(smem_addr(xbar), 0, ctl, 540)) break;
 #pragma unroll
               for (int i = 0; i < HR; ++i)
                 if (hw + 6 * i < t.nvalid)
 #pragma unroll
-                  for (int k = 0; k < S; ++k) amax[i] = fmaxf(amax[i], x[k * MR + hw + 6 * i]);
+                  for (int k = 0; k < S; ++k) amax[i] = fmaxf(amax[i], xch[k * MR + hw + 6 * i]);
             }
 #pragma unroll
             for (int i = 0; i < HR; ++i) {
@@ -865,9 +866,9 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
       const int dst = park[0], nt = park[1];  // output row, negative: none
       if constexpr (SWIGLU) {
         // h in place of the gate values, and its largest magnitude over the
-        // block's 128 columns (PARTS here, in each of S CTAs).  Two exchange
-        // buffers: who writes one again has seen everyone arrive for the other,
-        // and they arrive after their reads.
+        // block's 128 columns (PARTS here, in each of S CTAs).  A CTA by itself
+        // has two exchange buffers: who writes one again has seen everyone arrive
+        // for the other, and they arrive after their reads.
         const int n0 = nt * 128 + rank * C::WBOX + part * HP;
         float amax = 0.f;
 #pragma unroll
@@ -876,7 +877,8 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           v[j].y = silu_mul(v[j].y, v[HP / 2 + j].y);
           if (n0 + 2 * j < a.N) amax = fmaxf(amax, fmaxf(fabsf(v[j].x), fabsf(v[j].y)));
         }
-        float* x = xch + (local & 1u) * (C::PARTS * S * MR);
+        const uint32_t turn = S > 1 ? 0 : local & 1u;
+        float* x = xch + turn * C::XCH;
         float* mine = x + (C::PARTS * rank + part) * MR + place;
         if constexpr (S > 1) {
 #pragma unroll
@@ -889,7 +891,7 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
           if (S > 1) cluster_arrive(cluster_map(smem_addr(xbar), lane));
           else bar_arrive(smem_addr(xbar));
         }
-        if (!bar_wait<(S > 1)>(smem_addr(xbar), local & 1u, ctl, 540)) break;
+        if (!bar_wait<(S > 1)>(smem_addr(xbar), turn, ctl, 540)) break;
 #pragma unroll
         for (int k = 0; k < C::PARTS * S; ++k) amax = fmaxf(amax, x[k * MR + place]);
         if (dst >= 0 && n0 < a.N) {
@@ -965,6 +967,7 @@ cudaError_t launch_kernel(const Fp8GemmArgs& a, long long max_tiles, cudaStream_
   }
   cudaLaunchConfig_t cfg = {};
   const long long most = device_info().sm_count / C::S;
+  if (C::S > 1 && max_tiles > most) return cudaErrorInvalidValue;  // a cluster exchanges its maxima once
   cfg.gridDim = dim3(unsigned((max_tiles < most ? max_tiles : most) * C::S));
   cfg.blockDim = dim3(C::THREADS);
   cfg.dynamicSmemBytes = smem;
@@ -1001,9 +1004,9 @@ cudaError_t pick(const Fp8GemmArgs& a, bool swiglu, cudaStream_t st) {
   const long long rt = a.offsets ? groups + a.P / MR : (a.P + MR - 1) / MR;
   if (swiglu) {
     const long long t = rt * ((a.N + 127) / 128);
-    // a cluster shares a block of 128 columns while all clusters fit at once (T =
-    // 1, one expert of I = 2048, H = 4096: 10.0 us with 4 CTAs, 12.3 with 2, 17.0
-    // with 1, 18.6 with 8; T = 1, k = 4: 17.6 with 2, 18.8 with 1)
+    // a cluster shares a block of 128 columns while all clusters fit at once, one
+    // tile each (T = 1, one expert of I = 2048, H = 4096: 10.0 us with 4 CTAs, 12.3
+    // with 2, 17.0 with 1, 18.6 with 8; T = 1, k = 4: 17.6 with 2, 18.8 with 1)
     if (t * 4 <= sms) return launch<true, 64, MR>(a, t, st);
     if (t * 2 <= sms) return launch<true, 128, MR>(a, t, st);
     return launch<true, 256, MR>(a, t, st);
