@@ -665,7 +665,6 @@ __global__ void __launch_bounds__(Cfg<SWIGLU, BN, MR, SECTORS>::THREADS, 1)
     Ring<C::BUFS> acc;
     Ring<C::SLOTS> slot;
     uint32_t local = 0;  // tiles so far
-    bool ok = true;
     // column of this part's value o (swiglu: its gate, then its up columns)
     constexpr int HP = C::CP / 2;
     auto at = [&](int o) { return SWIGLU ? (o < HP ? o : BN / 2 + o - HP) + part * HP : part * C::CP + o; };

@@ -37,9 +37,6 @@ MOE_DEBUG_STARVE_FIRST_WAIT = 1
 #: smallest workspace of the 8-bit operators
 MOE_FP8_STATUS_BYTES = 128
 
-#: element types of the 8-bit operators' 16- and 32-bit tensors
-MOE_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-
 #: every symbol include/moe.h declares
 EXPORTS = (
     "moe_workspace_bytes", "moe_workspace_init", "moe_route_topk", "moe_bucket",
