@@ -17,6 +17,10 @@ norm      The sum of squares has only positive terms and meets at most 16 fmas
 codes     A code is off by half a step: 2^-4 of the value, 2^-10 of the scale
           below the normal range; plus the value's own error.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -752,3 +756,241 @@ def test_swiglu_silu_over_the_range(rows):
     want = np.abs(F.silu(gate)) * 2.0 ** 20 * down[:, None]
     err = np.abs(f64(s) * F.MAX / want - 1)
     assert err.max() <= 16 * U, (float(err.max() / U), float(gate.reshape(-1)[err.argmax()]))
+
+
+# ------------------------------------------------------- paths of few calls ---
+@pytest.mark.parametrize("T,k,E,N,K", [
+    (5, 8, 256, 1000, 512),    # 128-column tiles, two K blocks a stage
+    (5, 8, 256, 1000, 640),    # the same, a short last stage
+    (12, 4, 64, 136, 640),     # 64-column tiles, four K blocks a stage, a short last stage
+    (12, 4, 64, 136, 1024),    # the same, whole stages
+    (40, 1, 5, 200, 384),      # buckets of several tiles
+])
+@pytest.mark.parametrize("scatter", [False, True])
+def test_grouped_rows_in_order_several_blocks_per_copy(T, k, E, N, K, scatter):
+    """Small buckets of rows in bucket order, K of whole blocks: a stage's rows
+    are one copy, at the tile's first row."""
+    rng = np.random.default_rng(T + E + K)
+    off, ent = routing(rng, T, k, E)
+    P = T * k
+    assert 16 <= P <= 8 * E and K % 128 == 0
+    aq, as_ = rows8(rng, P, K)
+    wq, ws_ = mats8(rng, E, N, K)
+    ws = make_ws()
+    out = torch.empty(P, N, device="cuda")
+    moe.moe_grouped_gemm_fp8(dev(aq), dev(as_), dev(wq), dev(ws_), dev(off), dev(ent), out, ws, scatter=scatter)
+    assert moe.moe_get_error(ws) == 0
+    want, mag = F.grouped(F.dequant_rows(aq, as_), F.dequant_mats(wq, ws_), off, ent, 0)
+    check_prod(out[dev(ent).long()] if scatter else out, want, mag, K, F32)
+
+
+@pytest.mark.parametrize("P,E,I,H", [(20, 4, 256, 640), (24, 4, 1280, 384), (40, 5, 4096, 512), (16, 1, 272, 640),
+                                     (16, 1, 8192, 256)])
+def test_swiglu_rows_in_order_several_blocks_per_copy(P, E, I, H):
+    """The same for the pair, in clusters of 4, 2 and 1; E = 1 without offsets."""
+    rng = np.random.default_rng(P + I)
+    off, ent = routing(rng, P, 1, E)
+    aq, as_ = rows8(rng, P, H, spread=1)
+    gq, gs = mats8(rng, E, I, H)
+    uq, us = mats8(rng, E, I, H)
+    gs *= 2.0 ** -3
+    ws = make_ws()
+    q = torch.empty(P, I, dtype=torch.uint8, device="cuda")
+    s = torch.empty(P, F.blocks(I), device="cuda")
+    moe.moe_grouped_swiglu_fp8(*(dev(t) for t in (aq, as_, gq, gs, uq, us)), dev(off) if E > 1 else None, None, q, s, ws)
+    assert moe.moe_get_error(ws) == 0
+    h, dh = swiglu_ref(F.dequant_rows(aq, as_), F.dequant_mats(gq, gs), F.dequant_mats(uq, us), off, ent, 0, H)
+    check_codes(q, s, h, dh)
+
+
+@pytest.mark.parametrize("T,k", [(5, 4), (16, 2)])
+def test_expert_ffn_whole_blocks(T, k):
+    """I and H of whole blocks, with the shared expert: the down projection's
+    rows, and at T = 16 the shared expert's, come several K blocks per copy."""
+    rng = np.random.default_rng(T)
+    H, I, E = 384, 256, 16
+    x, xs = rows8(rng, T, H, spread=1)
+    off, ent = routing(rng, T, k, E)
+    parts = []
+    for n in (E, 1):
+        g, u, d = mats8(rng, n, I, H), mats8(rng, n, I, H), mats8(rng, n, H, I)
+        parts.append(dict(gate_q=g[0], gate_s=g[1] / 8, up_q=u[0], up_s=u[1], down_q=d[0], down_s=d[1]))
+    ex, sh = (moe.Fp8Experts(**{n: dev(t) for n, t in p.items()}) for p in parts)
+    shape = moe.shape_of(T, H, I, E, k)
+    ws = moe.fp8_workspace(shape, True)
+    partial = torch.empty(T * (k + 1), H, device="cuda")
+    moe.moe_expert_ffn_fp8(ex, sh, dev(x), dev(xs), dev(off), dev(ent), shape, partial, ws)
+    assert moe.moe_get_error(ws) == 0
+    a, want = F.dequant_rows(x, xs), np.zeros((T * (k + 1), H))
+    groups = ((parts[0], off, ent, k, ent), (parts[1], np.array([0, T]), np.arange(T), 0, np.arange(T * k, T * k + T)))
+    for p, offs, ents, div, rows in groups:
+        g, u, d = (F.dequant_mats(p[n + "_q"], p[n + "_s"]) for n in ("gate", "up", "down"))
+        h = F.silu(F.grouped(a, g, offs, ents, div)[0]) * F.grouped(a, u, offs, ents, div)[0]
+        want[rows] = F.grouped(F.dequant_rows(*F.quantise(h)), d, offs, ents, 0)[0]
+    # h is quantised on both sides: a value next to a border may take the other
+    # code, the bar of the layer test above
+    assert rel_l2_rows(f64(partial), want).max() < 5e-3
+
+
+@pytest.mark.parametrize("rows,N,K", [(3, 200, 65536), (16, 72, 7168), (40, 136, 16400), (150, 136, 7168)])
+def test_gemm_long_k(rows, N, K):
+    rng = np.random.default_rng(K)
+    aq, as_ = rows8(rng, rows, K)
+    wq, ws_ = mats8(rng, 1, N, K)
+    out = torch.empty(rows, N, device="cuda")
+    ws = make_ws()
+    moe.moe_gemm_fp8(dev(aq), dev(as_), dev(wq[0]), dev(ws_[0]), out, ws)
+    assert moe.moe_get_error(ws) == 0
+    want, mag = F.gemm(F.dequant_rows(aq, as_), F.dequant_mats(wq[0], ws_[0]))
+    check_prod(out, want, mag, K, F32)
+
+
+@pytest.mark.parametrize("T,k,E,K", [(5, 2, 8, 7168), (90, 2, 4, 7184)])
+def test_grouped_and_swiglu_long_k(T, k, E, K):
+    rng = np.random.default_rng(T + K)
+    off, ent = routing(rng, T, k, E)
+    aq, as_ = rows8(rng, T, K, spread=1)
+    gq, gs = mats8(rng, E, 144, K)
+    uq, us = mats8(rng, E, 144, K)
+    gs *= 2.0 ** -5
+    ws = make_ws()
+    a, g, u = F.dequant_rows(aq, as_), F.dequant_mats(gq, gs), F.dequant_mats(uq, us)
+    args = [dev(t) for t in (aq, as_, gq, gs, uq, us)]
+    out = torch.empty(T * k, 144, device="cuda")
+    moe.moe_grouped_gemm_fp8(*args[:4], dev(off), dev(ent), out, ws, a_div=k, scatter=True)
+    q = torch.empty(T * k, 144, dtype=torch.uint8, device="cuda")
+    s = torch.empty(T * k, 2, device="cuda")
+    moe.moe_grouped_swiglu_fp8(*args, dev(off), dev(ent), q, s, ws, a_div=k)
+    assert moe.moe_get_error(ws) == 0
+    want, mag = F.grouped(a, g, off, ent, k)
+    check_prod(out[dev(ent).long()], want, mag, K, F32)
+    check_codes(q, s, *swiglu_ref(a, g, u, off, ent, k, K))
+
+
+# --------------------------------------------------------------- non-finite ---
+@pytest.mark.parametrize("T,k,E,N,K", [(5, 8, 256, 200, 512), (6, 2, 16, 136, 272), (77, 2, 8, 200, 400),
+                                       (300, 4, 8, 136, 272)])
+def test_grouped_nan_stays_in_its_rows(T, k, E, N, K):
+    """Rows full of NaN beside clean ones, in 16-row tiles (whose MMAs read past
+    their rows), half tiles and full ones: every clean row is right."""
+    rng = np.random.default_rng(T + K)
+    off, ent = routing(rng, T, k, E)
+    P = T * k
+    aq, as_ = rows8(rng, P, K)
+    sick = rng.random(P) < 0.6
+    aq[sick] = 0x7F
+    as_[sick & (np.arange(P) % 2 == 0)] = np.inf
+    wq, ws_ = mats8(rng, E, N, K)
+    ws = make_ws()
+    out = torch.empty(P, N, device="cuda")
+    moe.moe_grouped_gemm_fp8(dev(aq), dev(as_), dev(wq), dev(ws_), dev(off), dev(ent), out, ws)
+    assert moe.moe_get_error(ws) == 0
+    aq[sick], as_[sick] = 0, 0
+    want, mag = F.grouped(F.dequant_rows(aq, as_), F.dequant_mats(wq, ws_), off, ent, 0)
+    check_prod(out[dev(~sick)], want[~sick], mag[~sick], K, F32)
+    assert np.isnan(f64(out)[sick]).all()
+
+
+@pytest.mark.parametrize("rows", [3, 40, 150])
+def test_swiglu_nonfinite_gates(rows):
+    """NaN and infinite gates and ups, block by block, and gates far below zero.
+    A NaN stays in its place and out of the maximum; an infinite maximum makes
+    the scale infinite, finite codes 0 and the infinite ones NaN."""
+    I, H = 7 * 128, 128
+    gq, uq = np.zeros((1, I, H)), np.zeros((1, I, H))
+    j = np.arange(128)
+    col = lambda b: slice(128 * b, 128 * b + 128)  # noqa: E731
+    gate = np.stack([(j % 7 - 3.0) / 2] * 7)       # gates of the blocks
+    up = np.stack([(j % 9 - 4.0) / 4] * 7)
+    gs, us = np.ones((1, 7, 1), np.float32), np.ones((1, 7, 1), np.float32)
+    gate[1, 17] = np.nan
+    up[2, 90] = np.nan
+    gs[0, 3] = np.inf            # +inf, -inf and, where the gate's code is 0, NaN
+    us[0, 4] = np.inf
+    gate[5] = -1.0
+    gs[0, 5] = 200.0             # silu counts as 0, beside ...
+    gate[5, 3], up[5, 3] = 0.25, 1.0  # ... one gate of 50
+    gate[6] = 1.0
+    gs[0, 6] = 3e38              # silu the identity, h infinite where |up| exceeds 1
+    up[6, 100] = 1.5
+    up[6, 101] = 0.5
+    aq = np.zeros((rows, H))
+    aq[:, 3] = 1.0
+    for b in range(7):
+        gq[0, col(b), 3], uq[0, col(b), 3] = gate[b], up[b]
+    args = [F.encode(aq), np.ones((rows, 1), np.float32), F.encode(gq), gs, F.encode(uq), us]
+    q = torch.empty(rows, I, dtype=torch.uint8, device="cuda")
+    s = torch.empty(rows, 7, device="cuda")
+    ws = make_ws()
+    moe.moe_grouped_swiglu_fp8(*(dev(t) for t in args), None, None, q, s, ws)
+    assert moe.moe_get_error(ws) == 0
+    with np.errstate(all="ignore"):
+        g = F.decode(args[2])[0, :, 3] * np.repeat(gs.reshape(-1).astype(np.float64), 128)
+        u = F.decode(args[4])[0, :, 3] * np.repeat(us.reshape(-1).astype(np.float64), 128)
+        h = F.silu(g) * u
+        h = np.where(np.abs(h) > np.finfo(np.float32).max, np.copysign(np.inf, h), h)
+        h = np.where(g < -88.8, h * 0, h)          # silu counts as 0 there
+        want_s = F.scales(h[None])[0]
+        t = h / np.repeat(want_s, 128)
+    assert np.isinf(want_s[[3, 4, 6]]).all() and np.isfinite(want_s[[0, 1, 2, 5]]).all()
+    got_s, got = f64(s), F.decode(codes_np(q))
+    for r in range(rows):
+        assert (np.abs(got_s[r, [0, 1, 2, 5]] / want_s[[0, 1, 2, 5]] - 1) <= 18 * U).all()
+        assert np.isposinf(got_s[r, [3, 4, 6]]).all()
+        np.testing.assert_array_equal(np.isnan(got[r]), np.isnan(t))
+        fine = ~np.isnan(t)
+        # half a step, and the quotient's own 20 units
+        tol = np.maximum(np.abs(t[fine]) * (2.0 ** -4 + 20 * U), 2.0 ** -10)
+        assert (np.abs(got[r][fine] - t[fine]) <= tol).all()
+
+
+def test_norm_rows_past_float32_come_out_as_zeros():
+    rng = np.random.default_rng(7)
+    for dt in (BF16, F32):
+        x = dev(rng.standard_normal((4, 512)), dt)
+        x[1] *= 1e30
+        x[2, 40] = 3e38
+        q, s, _, y = run_norm(x, None, torch.ones(512, device="cuda"), dt)
+        for r in (1, 2):
+            assert (f64(y)[r] == 0).all() and (f64(s)[r] == F.MIN_SCALE).all()
+            assert (F.decode(codes_np(q))[r] == 0).all()
+        good = [0, 3]
+        _, n = F.rmsnorm(f64(x)[good], None, np.ones(512), 1e-6)
+        check_codes(q[good], s[good], n, 40 * U * np.abs(n))
+
+
+def test_first_call_of_a_process_may_be_captured():
+    """No call before the captured one: whatever is set up once is set up under
+    capture."""
+    code = """
+import torch
+from routed_expert_ffn_fp32_b200 import moe
+g = torch.Generator(device="cuda").manual_seed(1)
+ints = lambda *s: torch.randint(0, 96, s, generator=g, dtype=torch.uint8, device="cuda")
+ones = lambda *s: torch.ones(s, device="cuda")
+aq, w, u = ints(5, 256), ints(1, 256, 256), ints(1, 256, 256)
+ws = torch.zeros(256, dtype=torch.uint8, device="cuda")
+x, nq, ns = torch.randn(5, 256, generator=g, device="cuda"), ints(5, 256), ones(5, 2)
+out, q, s = ones(5, 256), ints(5, 256), ones(5, 2)
+
+def calls():
+    moe.moe_rmsnorm_quant_fp8(x, weight, 1e-6, nq, ns)
+    moe.moe_gemm_fp8(aq, sc, w[0], wsc[0], out, ws)
+    moe.moe_grouped_swiglu_fp8(aq, sc, w, wsc, u, wsc, None, None, q, s, ws)
+
+weight, sc, wsc = ones(256), ones(5, 2), ones(1, 2, 2)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    calls()
+graph.replay()
+torch.cuda.synchronize()
+first = [t.clone() for t in (nq, ns, out, q, s)]
+calls()
+assert moe.moe_get_error(ws) == 0
+assert all(torch.equal(a, b) for a, b in zip(first, (nq, ns, out, q, s)))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
