@@ -994,3 +994,78 @@ print("same")
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("rows,N,dt", [(40, 256, F32), (700, 1600, BF16), (1300, 4096, F16), (3, 256, BF16)])
+def test_gemm_output_at_16_byte_alignment(rows, N, dt):
+    """Rows of whole 32-byte sectors that start in the middle of one; the values
+    around the output are left alone."""
+    rng = np.random.default_rng(rows)
+    K = 256
+    aq, as_ = rows8(rng, rows, K)
+    wq, ws_ = mats8(rng, 1, N, K)
+    shift = 16 // torch.empty(0, dtype=dt).element_size()
+    buf = torch.full((rows * N + 2 * shift,), 7.0, dtype=dt, device="cuda")
+    out = buf[shift:shift + rows * N].view(rows, N)
+    assert out.data_ptr() % 32 == 16
+    ws = make_ws()
+    moe.moe_gemm_fp8(dev(aq), dev(as_), dev(wq[0]), dev(ws_[0]), out, ws)
+    assert moe.moe_get_error(ws) == 0
+    want, mag = F.gemm(F.dequant_rows(aq, as_), F.dequant_mats(wq[0], ws_[0]))
+    check_prod(out, want, mag, K, dt)
+    assert (buf[:shift] == 7.0).all() and (buf[-shift:] == 7.0).all()
+
+
+@pytest.mark.parametrize("P,E", [(6, 4), (400, 4)])
+def test_empty_buckets_write_nothing(P, E):
+    """Pairs that lie in no bucket (a rank that holds none of their experts)."""
+    N, K = 256, 128
+    ints = torch.full((E, N, K), 0x38, dtype=torch.uint8, device="cuda")
+    one = torch.ones(E, 2, 1, device="cuda")
+    a, as_ = ints.view(-1, K)[:P].contiguous(), torch.ones(P, 1, device="cuda")
+    ent = torch.arange(P, dtype=torch.int32, device="cuda")
+    out = torch.full((P, N), 5.0, device="cuda")
+    q, s = torch.full((P, N), 0x11, dtype=torch.uint8, device="cuda"), torch.full((P, 2), -1.0, device="cuda")
+    ws = make_ws()
+    for at in (0, P // 2, P):
+        off = torch.full((E + 1,), at, dtype=torch.int32, device="cuda")
+        moe.moe_grouped_gemm_fp8(a, as_, ints, one, off, ent, out, ws, scatter=True)
+        moe.moe_grouped_swiglu_fp8(a, as_, ints, one, ints, one, off, ent, q, s, ws, a_div=1)
+    assert moe.moe_get_error(ws) == 0
+    assert (out == 5.0).all() and (q == 0x11).all() and (s == -1.0).all()
+
+
+def test_swiglu_results_repeat_beside_other_calls():
+    """The same call alone, again, and while calls of other shapes run on a second
+    stream over the same workspace: the same bits."""
+    rng = np.random.default_rng(31)
+    T, k, E, I, H = 300, 4, 16, 640, 384
+    aq, as_ = rows8(rng, T, H, spread=1)
+    mats = [dev(t) for t in (*mats8(rng, E, I, H), *mats8(rng, E, I, H))]
+    mats[1] /= 8
+    ws = make_ws()
+    other = _prefill(5, 40, 512, 512)
+    calls = []
+    for rows in (T, 2):   # full tiles, and a cluster's
+        o, e = routing(rng, rows, k, E)
+        args = [dev(aq[:rows]), dev(as_[:rows]), *mats, dev(o), dev(e)]
+        q = torch.empty(rows * k, I, dtype=torch.uint8, device="cuda")
+        calls.append((args, q, torch.empty(rows * k, 5, device="cuda")))
+    first = []
+    for args, q, s in calls:
+        moe.moe_grouped_swiglu_fp8(*args, q, s, ws, a_div=k)
+        torch.cuda.synchronize()
+        first.append((q.clone(), s.clone()))
+    side = torch.cuda.Stream()
+    for _ in range(20):
+        for (args, q, s), (q0, s0) in zip(calls, first):
+            q.zero_()
+            s.zero_()
+            with torch.cuda.stream(side):
+                moe.moe_gemm_fp8(*other[0], other[1], ws)
+            moe.moe_grouped_swiglu_fp8(*args, q, s, ws, a_div=k)
+            with torch.cuda.stream(side):
+                moe.moe_gemm_fp8(*other[0], other[1], ws)
+            torch.cuda.synchronize()
+            assert torch.equal(q, q0) and torch.equal(s, s0)
+    assert moe.moe_get_error(ws) == 0
