@@ -351,10 +351,13 @@ MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_
  *
  * The last block of a dimension may be short.  A value is code times scale; a
  * product sums each block of 128 in the tensor core's float32 accumulator and
- * the blocks, times both scales, in float32, in ascending order.  Quantised outputs
- * take s = max(max|v| / 448, 2^-126) over a block's values that are not NaN,
- * and code = E4M3(v / s): the quotient rounded to float32, then to E4M3, both to
- * nearest even; a NaN stays NaN.
+ * the blocks, times both scales, in float32, in ascending order.  The two scales
+ * are multiplied first, in float32: where that product leaves float32's normal
+ * range (a row at the smallest scale, 2^-126, times a weight scale below 1), the
+ * block's sum is less exact, down to 0, or not finite.  Quantised outputs take s =
+ * max(max|v| / 448, 2^-126) over a block's values that are not NaN, and code =
+ * E4M3(v / s): the quotient rounded to float32, then to E4M3, both to nearest
+ * even; a NaN stays NaN.
  *
  * K (and the width of quantised outputs) is a multiple of 16 in [16, 65536],
  * N in [1, 65536], rows up to 2^21, E up to 1024; pointers 16-byte aligned.
@@ -362,8 +365,9 @@ MOE_API moe_status_t moe_decode_mxfp4(const uint8_t* q, const uint8_t* s, int32_
  * (moe_workspace_init) of at least MOE_FP8_STATUS_BYTES bytes that holds the
  * latched error, the wait limit and the debug switch (moe_get_error,
  * moe_workspace_set_limits; limits below 20 us count as 20; the switch holds
- * back the first block's scales) and no scratch: calls on different streams may share it unless stated
- * otherwise.  Outputs must not overlap inputs unless stated otherwise.
+ * back the first block's scales) and no scratch: calls on different streams may
+ * share it unless stated otherwise.  Outputs must not overlap inputs unless
+ * stated otherwise.
  * ------------------------------------------------------------------------- */
 #define MOE_FP8_STATUS_BYTES 128
 
@@ -392,7 +396,8 @@ typedef struct moe_fp8_experts {
  * everything is computed in float32 from the inputs and each output is rounded
  * once (the norm sees the sum before it is rounded to residual_out).
  * residual_out may be residual or x itself, y_out may be x.  16 <= H <= 16384,
- * H % 16 == 0.  A row whose sum of squares exceeds float32 comes out as zeros. */
+ * H % 16 == 0.  A row whose sum of squares exceeds float32 comes out as zeros;
+ * with eps = 0, one whose squares vanish in float32 is not finite. */
 MOE_API moe_status_t moe_rmsnorm_quant_fp8(const void* x, const void* residual, const float* weight,
                                            int32_t rows, int32_t H, int32_t dtype, float eps,
                                            void* residual_out, void* y_out, uint8_t* q_out,

@@ -34,9 +34,9 @@
 // FMAs saves 10 us, the scales 10 us).  Grouped products of many experts are
 // bound by HBM: down, T = 5, k = 8, 256 experts, H = 4096, I = 2048: 53 us for
 // 316 MB (6.0 TB/s); T = 2048: 380 us (6.1 TB/s); gate / up T = 1: 26.3 us for
-// 134 MB (5.1 TB/s), T = 2048: 850 us (5.1 TB/s, TMA row gather and the tile's
-// end beside the weights).  Under a sustained load the card's power limit lowers
-// the clock, and the full tiles follow it (162, 447 and 910 us).
+// 134 MB (5.1 TB/s), T = 2048: 755 to 890 us (up to 5.7 TB/s, TMA row gather and
+// the tile's end beside the weights).  Under a sustained load the card's power limit
+// lowers the clock, and the full tiles follow it (161, 460 and 915 us).
 //
 // Few rows mean few tiles, so the tile gets narrower (down to 64 weight rows)
 // to spread the weights over more SMs; K is never split, so nothing has to be
@@ -1015,10 +1015,10 @@ cudaError_t pick(const Fp8GemmArgs& a, bool swiglu, cudaStream_t st) {
   // gains (T = 1, N = 4096, K = 2048: 9.2 us at 16 columns, 7.3 at 32, 6.6 at
   // 64, 7.3 at 128).  Small buckets stream weights: 128 columns once the tiles
   // outnumber the SMs (T = 5, k = 8, 256 experts of N = 4096, K = 2048: 55.2 us
-  // at 64, 51.6 at 128, 54.7 at 256).  Full tiles take the widest that still
-  // fills the SMs, or the narrowest that fits them at once (T = 300, N = 2048,
-  // K = 4096: 12.8 us at 64, 15.2 at 128; T = 512, N = 4096: 21.7 at 64, 17.0 at
-  // 128, 20.1 at 256).
+  // at 64, 51.6 at 128, 54.7 at 256).  Full tiles take the narrowest whose tiles
+  // all fit the SMs at once, and 256 columns where none do (T = 300, N = 2048, K =
+  // 4096: 12.8 us at 64, 15.2 at 128; T = 512, N = 4096: 21.7 at 64, 17.0 at 128,
+  // 20.1 at 256).
   auto tiles = [&](int bn) { return rt * ((a.N + bn - 1) / bn); };
   if constexpr (MR == 16) {
     return tiles(128) > sms ? launch<false, 128, MR>(a, tiles(128), st) : launch<false, 64, MR>(a, tiles(64), st);
