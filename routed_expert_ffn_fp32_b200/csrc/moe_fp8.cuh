@@ -55,8 +55,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
 // units before the last rounding.  The quotients of float32 values that lie so
 // near to where the float32 next to a code's border begins are few enough to be
 // enumerated (tests/test_fp8_host.py), and all of them round as v / s does.  In
-// pairs it costs the norm 1 to 5 % (T = 4096, H = 4096: 27.1 -> 27.5 us; T = 777,
-// H = 7088: 7.2 -> 7.5) and gate / up nothing to speak of; the division itself
+// pairs it costs the norm 1 to 3 % (T = 4096, H = 4096: 27.1 -> 27.4 us; T = 777,
+// H = 7088: 7.1 -> 7.3) and gate / up nothing to speak of; the division itself
 // cost 10 to 35 % and 10 % (29.9, 9.5 us; T = 2048: 860 -> 945 us).
 struct Fp8Quotient {
   float s, r;
@@ -76,7 +76,7 @@ struct Fp8Quotient {
   // (product less value, times -r: a negative zero keeps its sign)
   __device__ __forceinline__ float2 operator()(float2 v) const {
     const float2 t = mul2(v, make_float2(r, r));
-    return fma2(fma2(t, make_float2(s, s), mul2(v, make_float2(-1.f, -1.f))), make_float2(-r, -r), t);
+    return fma2(fma2(t, make_float2(s, s), make_float2(-v.x, -v.y)), make_float2(-r, -r), t);
   }
 };
 // Codes of N pairs of values over their scale, two pairs to a word
