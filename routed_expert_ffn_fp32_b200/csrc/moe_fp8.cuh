@@ -48,41 +48,34 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
   return unpack2(r);
 }
 
-// Quotients of a block's values by its scale s, as its codes need them: v * (1 /
+// Quotients of a block's values by its scale s, as its codes need them.  v * (1 /
 // s) is up to 1.5 units off, which next to a rounding border is the neighbouring
-// code.  The residual's correction (P. Markstein, "Computation of elementary
-// functions on the IBM RISC System/6000 processor", 1990) leaves it within 2^-22
-// units before the last rounding.  The quotients of float32 values that lie so
-// near to where the float32 next to a code's border begins are few enough to be
-// enumerated (tests/test_fp8_host.py), and all of them round as v / s does.  In
-// pairs it costs the norm 1 to 3 % (T = 4096, H = 4096: 27.1 -> 27.4 us; T = 777,
-// H = 7088: 7.1 -> 7.3) and gate / up nothing to speak of; the division itself
-// cost 10 to 35 % and 10 % (29.9, 9.5 us; T = 2048: 860 -> 945 us).
+// code.  With h = 1 / s rounded and e = 1 - h s, which is exact, 1 / s = h / (1 - e),
+// so v / s is v h + v h (e + e^2) to within 3 * 2^-24 units before the sum's one
+// rounding.  The quotients of float32 values that lie so near to where the float32
+// next to a code's border begins are few enough to be enumerated
+// (tests/test_fp8_host.py), and all of them round as v / s does.  Nothing leaves
+// float32's range: h is normal, and the products are of the codes' size.  In pairs
+// it costs the norm 1 to 9 % (T = 4096, H = 4096: 27.1 -> 27.6 us; T = 777, H =
+// 7088, codes only: f16 7.1 -> 7.5, f32 8.4 -> 9.1) and gate / up nothing to speak
+// of; the division cost 10 to 35 % and 10 % (29.9, 9.5 us; T = 2048: 860 -> 945 us).
 struct Fp8Quotient {
-  float s, r;
-  // Brings scales whose residuals would leave float32's range to ones that do
-  // not, and the values with them.  An infinite scale: finite values give 0,
-  // infinite ones NaN.
-  template <int N>
-  __device__ __forceinline__ Fp8Quotient(float scale, float2 (&v)[N]) : s(scale) {
-    if (s < 0x1p-80f) {
-      s *= 0x1p64f;
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = mul2(v[i], make_float2(0x1p64f, 0x1p64f));
-    }
-    r = 1.f / s;
-    if (r == 0.f) s = 0.f;
+  float h, e;
+  __device__ __forceinline__ explicit Fp8Quotient(float s) : h(1.f / s) {
+    const float d = fmaf(-h, s, 1.f);
+    e = h == 0.f ? 0.f : fmaf(d, d, d);  // s infinite: finite values give 0, infinite ones NaN
   }
-  // (product less value, times -r: a negative zero keeps its sign)
   __device__ __forceinline__ float2 operator()(float2 v) const {
-    const float2 t = mul2(v, make_float2(r, r));
-    return fma2(fma2(t, make_float2(s, s), make_float2(-v.x, -v.y)), make_float2(-r, -r), t);
+    const float2 hh = make_float2(h, h);
+    const float2 q = fma2(v, hh, mul2(mul2(v, hh), make_float2(e, e)));
+    // (a negative zero's terms have opposite signs where e is negative)
+    return make_float2(copysignf(q.x, v.x), copysignf(q.y, v.y));
   }
 };
 // Codes of N pairs of values over their scale, two pairs to a word
 template <int N>
-__device__ __forceinline__ void fp8_codes(float2 (&v)[N], float scale, uint32_t (&q)[(N + 1) / 2]) {
-  const Fp8Quotient of(scale, v);
+__device__ __forceinline__ void fp8_codes(const float2 (&v)[N], float scale, uint32_t (&q)[(N + 1) / 2]) {
+  const Fp8Quotient of(scale);
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const float2 d = of(v[i]);

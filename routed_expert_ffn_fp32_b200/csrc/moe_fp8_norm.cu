@@ -6,7 +6,7 @@
 //
 // One CTA per row.  The row is read once into registers, so the traffic is the
 // algorithmic one: bf16 rows of 4096 with residual and all outputs move 9 bytes
-// a value, 151 MB at T = 4096, in 27.4 us (5.5 TB/s, 84 % of a plain copy).
+// a value, 151 MB at T = 4096, in 27.6 us (5.5 TB/s, 83 % of a plain copy).
 // Bound by HBM when rows are many, by two dependent memory latencies (row,
 // weight) and the launch when they are few (2.3 us at T = 1).
 // A thread owns 8 consecutive values per chunk (16-byte loads of 16-bit types),
@@ -74,8 +74,8 @@ struct Io<float> {
 };
 
 // WPR warps share a row, each thread holding NCH chunks of 8 values.  With two
-// chunks, registers for three CTAs per SM (two: T = 777, H = 7088, f16: 8.2 us
-// instead of 7.3).
+// chunks, registers for three CTAs per SM (two: T = 3000, H = 7088, bf16: 33.8 us
+// instead of 27.6, f32: 37.2 instead of 31.6).
 template <typename T, int WPR, int NCH>
 __global__ void __launch_bounds__(WPR * 32, NCH == 2 ? 3 : 1) k_norm_fp8(NormFp8Args a) {
   __shared__ float part[WPR];

@@ -197,21 +197,23 @@ def _rounded(x):
     return round(x / unit) * unit
 
 
-def test_corrected_quotients_round_as_the_division():
-    """The kernels' quotient: t = v r with r = 1 / s, then t - (t s - v) r, each
-    step rounded to float32.  Before its last rounding it is within 2.5 * 2^-24
-    units of v / s: t is within 1.5 (r's half unit counts below one, t's own half),
-    the correction takes r's relative error of 2^-24 of that and at most another
-    2^-24 from the residual's rounding.  A code changes only where the rounded
-    quotient crosses a border of five significant bits, that is, where v / s lies
-    that near to the middle between the border and the next float32: for v, s
-    as 24-bit whole numbers A, S and the middle m, where |A 2^k - m S| is a few
-    units.  As m is next to a multiple of 2^20, S has to be as well; all such S, m
-    and A are gone through (and quotients at random)."""
+def test_quotients_round_as_the_division():
+    """The kernels' quotient: with h = 1 / s and d = 1 - h s, both rounded to float32
+    (d is exact), e = d + d^2 and v h + (v h) e, each step rounded once.  As 1 / s =
+    h / (1 - d), before its last rounding it is off by the roundings of e, of v h
+    and of their product, each 2^-24 of a term of 2^-24, and by d^3: 3 * 2^-24
+    units at most.  A code changes only where the rounded quotient crosses a border
+    of five significant bits, that is, where v / s lies that near to the middle
+    between the border and the next float32: for v, s as 24-bit whole numbers A, S
+    and the middle m, where |A 2^k - m S| is a few units.  As m is next to a multiple
+    of 2^20, S has to be as well; all such S, m and A are gone through (and quotients
+    at random)."""
     def check(A, S):
-        r = _rounded(Fraction(1, S))
-        t = _rounded(A * r)
-        assert _rounded(t - _rounded(t * S - A) * r) == _rounded(Fraction(A, S)), (A, S)
+        h = _rounded(Fraction(1, S))
+        d = 1 - h * S
+        assert d == _rounded(d)
+        e = _rounded(d + d * d)
+        assert _rounded(A * h + _rounded(_rounded(A * h) * e)) == _rounded(Fraction(A, S)), (A, S)
 
     found = 0
     for S in (c * 2 ** 20 + d for c in range(8, 17) for d in range(-24, 25)):
